@@ -315,6 +315,54 @@ CCE_API cce_status_t cce_backward_shard(const void* E, const void* C_shard, cons
                                         int64_t v_offset, int64_t ignore_index, float filter_eps, float* dE_partial,
                                         float* dC_shard, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- Distillation from a teacher's top logits ----
+ * For a token with teacher entries (ids[i,k], teacher[i,k]), k < K, and a
+ * temperature T:
+ *     p[i,k] = softmax over the row's live entries of teacher[i,k] / T
+ *     lse[i] = log sum_v exp(z_iv / T),   z_iv = E_i . C_v over all of V
+ *     loss[i] = T^2 sum_k p[i,k] (log p[i,k] - z_{i, ids[i,k]} / T + lse[i]),
+ * the Kullback-Leibler divergence of the student's softmax from the teacher's
+ * distribution over its listed ids, times T^2.  An entry is not live, and its
+ * logit is not looked at, if its id is ignore_index; nor if its logit is
+ * -inf (then its id is not looked at).  A row without live entries has loss 0
+ * and no gradient.  An id that is listed twice counts twice.  A live entry
+ * with an id outside [0, V) or a NaN or +inf logit makes the row's loss NaN,
+ * sets status flag bit 1, and the row has no gradient.  The entries need no
+ * order.  1 <= K <= 1024; temperature finite and > 0.
+ * The N x V logits are not written to memory: the listed logits are taken
+ * from the tiles of the log-sum-exp pass.  ids is int64, teacher float or
+ * bf16 (cce_dtype_t). */
+typedef enum { CCE_DTYPE_F32 = 0, CCE_DTYPE_BF16 = 1 } cce_dtype_t;
+
+/* Workspace bytes of cce_distill_forward / cce_distill_backward (0 if the
+ * sizes or flags are invalid; the forward's also without a usable device):
+ * the forward's partials (12 bytes per token and vocabulary split) and
+ * 8 K + 8 bytes per token; the backward's stripes as for CCE_BWD_STRIPES,
+ * 8 K + 8 bytes per token and, with CCE_BWD_BF16_GRADS, the fp32 sums of dE
+ * (and of dC if it is accumulated into or N > 16384). */
+CCE_API size_t cce_distill_forward_workspace_size(int64_t N, int64_t D, int64_t V, int64_t K);
+CCE_API size_t cce_distill_backward_workspace_size(int64_t N, int64_t D, int64_t V, int64_t K, unsigned flags);
+
+/* Forward: loss [N] fp32 and lse [N] fp32 (of the logits divided by T; also
+ * for rows without a target).  Both are NaN if a bounded wait gave up. */
+CCE_API cce_status_t cce_distill_forward(const void* E, const void* C, const int64_t* ids, const void* teacher,
+                                         int teacher_dtype, int64_t N, int64_t D, int64_t V, int64_t K,
+                                         int64_t ignore_index, float temperature, float* loss, float* lse,
+                                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* Backward: gradients of sum_i dloss[i] * loss[i],
+ *     G[i,v] = dloss[i] T (exp(z_iv / T - lse[i]) - sum_{k: ids[i,k] = v} p[i,k]),
+ *     dE = G C,  dC = G^T E,
+ * through stripes of G as with CCE_BWD_STRIPES (no entry is filtered).  lse is
+ * cce_distill_forward's on the same inputs and temperature.  flags:
+ * CCE_BWD_DETERMINISTIC (dE summed in stripe order), CCE_BWD_BF16_GRADS,
+ * CCE_BWD_ACCUMULATE, with their meaning in cce_backward_ex. */
+CCE_API cce_status_t cce_distill_backward(const void* E, const void* C, const int64_t* ids, const void* teacher,
+                                          int teacher_dtype, const float* lse, const float* dloss, int64_t N,
+                                          int64_t D, int64_t V, int64_t K, int64_t ignore_index, float temperature,
+                                          unsigned flags, void* dE, void* dC, void* workspace,
+                                          size_t workspace_bytes, void* stream);
+
 /* Synchronises `stream`, then copies the status block of `workspace` (as left
  * by the last call that used it) into *out.  Returns CCE_ERR_TIMEOUT or
  * CCE_ERR_BAD_LABEL if the corresponding flag is set, else CCE_OK. */

@@ -14,6 +14,10 @@ Tensor helpers (torch supplies device memory and the current stream):
 forward(E, C, y) -> (loss, lse), backward(E, C, y, lse, dloss, filter_eps)
 -> (dE, dC), and linear_cross_entropy(E, C, y) for a mean-reduced loss with
 autograd.
+
+On the same head, also without N x V logits in memory: distill_forward,
+distill_backward and linear_distillation (the loss on a teacher's top logits
+and its gradients; cce_distill_forward, cce_distill_backward).
 """
 from __future__ import annotations
 
@@ -29,6 +33,8 @@ from ._native import (CCE_BWD_ACCUMULATE, CCE_BWD_BF16_GRADS, CCE_BWD_DETERMINIS
                       cce_debug_set_stripe_order,
                       cce_backward, cce_backward_ex, cce_backward_prepare,
                       cce_backward_shard, cce_backward_workspace_size, cce_backward_workspace_size_ex,
+                      CCE_DTYPE_BF16, CCE_DTYPE_F32, cce_distill_backward, cce_distill_backward_workspace_size,
+                      cce_distill_forward, cce_distill_forward_workspace_size,
                       cce_forward_shard, cce_merge_shards, cce_debug_forward_logits,
                       cce_debug_set_backward_trace, cce_debug_set_backward_variant, cce_debug_set_prefetch, cce_debug_set_forward_variant, cce_debug_set_kernel_events, cce_debug_set_wait_limit_ns,
                       cce_debug_withhold_loads, cce_forward, cce_forward_noalloc,
@@ -54,6 +60,9 @@ __all__ = [
     "load_library",
     "forward", "backward", "read_status", "linear_cross_entropy", "Workspace",
     "CCE_BWD_ROW_MAX", "cce_forward_ex", "cce_backward_prepare_rows",
+    "CCE_DTYPE_F32", "CCE_DTYPE_BF16", "cce_distill_forward", "cce_distill_backward",
+    "cce_distill_forward_workspace_size", "cce_distill_backward_workspace_size",
+    "distill_forward", "distill_backward", "linear_distillation",
 ]
 
 
@@ -218,6 +227,22 @@ def linear_cross_entropy(E, C, y, ignore_index: int = IGNORE_INDEX, filter_eps: 
     autograd support; the N x V logits are never materialised."""
     from ._autograd import LinearCrossEntropy
     return LinearCrossEntropy.apply(E, C, y, ignore_index, filter_eps)
+
+
+def linear_distillation(E, C, ids, teacher, temperature: float = 1.0, ignore_index: int = IGNORE_INDEX):
+    """Mean distillation loss (distill_forward) over the tokens that have a
+    teacher entry, with autograd support for E and C (bf16 gradients, each
+    sum rounded once); the N x V logits are never stored."""
+    from ._autograd import LinearDistillation
+    return LinearDistillation.apply(E, C, ids, teacher, temperature, ignore_index)
+
+
+def __getattr__(name):
+    # helpers that need torch at import time
+    if name in ("distill_forward", "distill_backward"):
+        from . import _distill
+        return getattr(_distill, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 # ---------------------------------------------------------------------------

@@ -12,6 +12,8 @@ import torch
 
 from . import backward as _cce_backward
 from . import forward as _cce_forward
+from ._distill import distill_backward as _distill_backward
+from ._distill import distill_forward as _distill_forward
 
 
 class LinearCrossEntropy(torch.autograd.Function):
@@ -33,3 +35,28 @@ class LinearCrossEntropy(torch.autograd.Function):
         dE, dC = _cce_backward(E.contiguous(), C.contiguous(), y.contiguous(), lse, dloss.contiguous(),
                                ctx.filter_eps, ctx.ignore_index, row_max=row_max)
         return dE.to(E.dtype), dC.to(C.dtype), None, None, None
+
+
+class LinearDistillation(torch.autograd.Function):
+    """Mean distillation loss over the tokens with a teacher entry; the
+    forward keeps the log-sum-exp (N floats) for the backward pass."""
+
+    @staticmethod
+    def forward(ctx, E, C, ids, teacher, temperature: float, ignore_index: int):
+        E, C, ids, teacher = E.contiguous(), C.contiguous(), ids.contiguous(), teacher.contiguous()
+        loss, lse = _distill_forward(E, C, ids, teacher, temperature, ignore_index)
+        keep = ((ids != ignore_index) & (teacher != float("-inf"))).any(1)
+        n = keep.sum()
+        ctx.save_for_backward(E, C, ids, teacher, lse, n)
+        ctx.temperature = temperature
+        ctx.ignore_index = ignore_index
+        return loss.sum() / n
+
+    @staticmethod
+    def backward(ctx, g):
+        E, C, ids, teacher, lse, n = ctx.saved_tensors
+        # rows without an entry have no gradient whatever their dloss
+        dloss = (g.to(torch.float32) / n).expand(E.shape[0]).contiguous()
+        dE, dC = _distill_backward(E, C, ids, teacher, lse, dloss, ctx.temperature, ctx.ignore_index, bf16_grads=True)
+        need = ctx.needs_input_grad
+        return dE if need[0] else None, dC if need[1] else None, None, None, None, None

@@ -69,6 +69,16 @@ def load_library():
         lib.cce_backward_shard.argtypes = [c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_i64, c_i64, c_f32,
                                            c_vp, c_vp, c_vp, c_size, c_vp]
         lib.cce_backward_shard.restype = ctypes.c_int
+        lib.cce_distill_forward_workspace_size.argtypes = [c_i64] * 4
+        lib.cce_distill_forward_workspace_size.restype = c_size
+        lib.cce_distill_backward_workspace_size.argtypes = [c_i64] * 4 + [ctypes.c_uint]
+        lib.cce_distill_backward_workspace_size.restype = c_size
+        lib.cce_distill_forward.argtypes = [c_vp, c_vp, c_vp, c_vp, ctypes.c_int, c_i64, c_i64, c_i64, c_i64, c_i64,
+                                            c_f32, c_vp, c_vp, c_vp, c_size, c_vp]
+        lib.cce_distill_forward.restype = ctypes.c_int
+        lib.cce_distill_backward.argtypes = [c_vp, c_vp, c_vp, c_vp, ctypes.c_int, c_vp, c_vp, c_i64, c_i64, c_i64,
+                                             c_i64, c_i64, c_f32, ctypes.c_uint, c_vp, c_vp, c_vp, c_size, c_vp]
+        lib.cce_distill_backward.restype = ctypes.c_int
         lib.cce_read_status.argtypes = [c_vp, c_vp, ctypes.POINTER(CCECounters)]
         lib.cce_read_status.restype = ctypes.c_int
         lib.cce_status_string.argtypes = [ctypes.c_int]
@@ -239,6 +249,38 @@ def cce_backward_shard(E: int, C_shard: int, y: int, lse: int, dloss: int, N: in
                                            filter_eps, dE_partial, dC_shard, workspace, workspace_bytes, stream)
     if check:
         _check(st, "cce_backward_shard")
+    return st
+
+
+CCE_DTYPE_F32 = 0
+CCE_DTYPE_BF16 = 1
+
+
+def cce_distill_forward_workspace_size(N: int, D: int, V: int, K: int) -> int:
+    return int(load_library().cce_distill_forward_workspace_size(N, D, V, K))
+
+
+def cce_distill_backward_workspace_size(N: int, D: int, V: int, K: int, flags: int) -> int:
+    return int(load_library().cce_distill_backward_workspace_size(N, D, V, K, flags))
+
+
+def cce_distill_forward(E: int, C: int, ids: int, teacher: int, teacher_dtype: int, N: int, D: int, V: int, K: int,
+                        ignore_index: int, temperature: float, loss: int, lse: int, workspace: int,
+                        workspace_bytes: int, stream: int, check: bool = True) -> int:
+    st = load_library().cce_distill_forward(E, C, ids, teacher, teacher_dtype, N, D, V, K, ignore_index, temperature,
+                                            loss, lse, workspace, workspace_bytes, stream)
+    if check:
+        _check(st, "cce_distill_forward")
+    return st
+
+
+def cce_distill_backward(E: int, C: int, ids: int, teacher: int, teacher_dtype: int, lse: int, dloss: int, N: int,
+                         D: int, V: int, K: int, ignore_index: int, temperature: float, flags: int, dE: int, dC: int,
+                         workspace: int, workspace_bytes: int, stream: int, check: bool = True) -> int:
+    st = load_library().cce_distill_backward(E, C, ids, teacher, teacher_dtype, lse, dloss, N, D, V, K, ignore_index,
+                                             temperature, flags, dE, dC, workspace, workspace_bytes, stream)
+    if check:
+        _check(st, "cce_distill_backward")
     return st
 
 

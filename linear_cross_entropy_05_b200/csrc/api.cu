@@ -45,6 +45,8 @@ cudaError_t launch_clear_visited_rows(unsigned long long* acc, int V, int D, con
 cudaError_t launch_flat_rows(const void* E, const void* C, const int64_t* y, const float* lse, const float* dloss,
                              const FlatArgs& f, cudaStream_t stream);
 cudaError_t launch_f32_to_bf16(const float* src, void* dst, size_t n, bool accumulate, int sms, cudaStream_t stream);
+cudaError_t launch_distill_targets(const TargetArgs& a, cudaStream_t stream);
+cudaError_t launch_distill_finalize(const DistillFinArgs& a, cudaStream_t stream);
 }  // namespace cce
 
 using namespace cce;
@@ -232,9 +234,11 @@ struct FwdPlan {
 };
 
 // The forward's launch plan for a GPU with `sms` SMs (host arithmetic only).
-bool plan_forward_for(int64_t N, int64_t D, int64_t V, int sms, FwdPlan* p) {
+// pairs_only: the CTA-pair kernel whatever the debug variant (distillation).
+bool plan_forward_for(int64_t N, int64_t D, int64_t V, int sms, FwdPlan* p, bool pairs_only = false) {
   if (!sizes_ok(N, D, V) || sms <= 0) return false;
-  p->pair = g_fwd_variant.load() == 1 && sms >= 2;
+  if (pairs_only && sms < 2) return false;
+  p->pair = (pairs_only || g_fwd_variant.load() == 1) && sms >= 2;
   const int rows = p->pair ? 2 * BM : BM;       // token rows per work unit
   const int workers = p->pair ? sms / 2 : sms;  // CTA pairs or CTAs
   p->n_mblk = (int)((N + rows - 1) / rows);
@@ -265,11 +269,11 @@ bool plan_forward_for(int64_t N, int64_t D, int64_t V, int sms, FwdPlan* p) {
   return true;
 }
 
-bool plan_forward(int64_t N, int64_t D, int64_t V, FwdPlan* p) {
+bool plan_forward(int64_t N, int64_t D, int64_t V, FwdPlan* p, bool pairs_only = false) {
   if (!sizes_ok(N, D, V)) return false;
   const DeviceInfo di = device_info();
   if (!di.ok || di.sms <= 0) return false;
-  return plan_forward_for(N, D, V, di.sms, p);
+  return plan_forward_for(N, D, V, di.sms, p, pairs_only);
 }
 
 // Backward workspace: status | pre-pass header | dC row bits [ceil(V/32)] |
@@ -376,6 +380,70 @@ bool plan_backward(int64_t N, int64_t D, int64_t V, BwdPlan* p, unsigned flags =
   return true;
 }
 
+// The sorted targets of a distillation call, in its workspace.
+struct TargetBuffers {
+  int* id;
+  float* w;
+  float* neg_entropy;
+  int* row_kind;
+  int K;
+};
+
+// The logit pass of the forward: launches the tile kernel, which leaves the
+// splits' partials behind the (zeroed) status block of the workspace.  tg:
+// distillation targets to pick (CTA-pair kernel), with each split's sum of
+// weight x logit going to `dot`.
+cce_status_t launch_logit_pass(const void* E, const void* C, int64_t N, int64_t D, int64_t V, const FwdPlan& p,
+                               void* ws, float* dbg_logits, cudaStream_t stream, const TargetBuffers* tg = nullptr,
+                               float* dot = nullptr, float scale2 = LOG2E) {
+  CUtensorMap tmE, tmC;
+  if (!make_map(&tmE, E, N, D, BM) || !make_map(&tmC, C, V, D, p.pair ? BM : BN)) return CCE_ERR_CUDA;
+
+  unsigned long long* status = reinterpret_cast<unsigned long long*>(ws);
+  float2* partial = reinterpret_cast<float2*>(reinterpret_cast<char*>(ws) + STATUS_BYTES);
+  FwdArgs a{};
+  a.N = (int)N;
+  a.D = (int)D;
+  a.V = (int)V;
+  a.n_mblk = p.n_mblk;
+  a.n_vtile = p.n_vtile;
+  a.n_split = p.n_split;
+  a.n_units = p.n_mblk * p.n_split;
+  a.group_m = p.group_m;
+  a.partial = partial;
+  a.dbg_logits = dbg_logits;
+  a.status = status;
+  a.wait_limit_ns = g_wait_limit_ns.load();
+  a.withhold_loads = g_withhold_loads.load();
+  a.pf = g_fwd_pf.load();
+  a.l2_hints = g_fwd_l2_hints.load();
+  if (tg) {
+    a.tgt_id = tg->id;
+    a.tgt_w = tg->w;
+    a.tgt_k = tg->K;
+    a.dot = dot;
+  }
+  a.scale2 = scale2;
+  a.sched = p.pair ? g_fwd_order.load() : 0;
+  if (a.sched) {
+    // which L2 half each SM is in: found once per device and process (the
+    // first launch on a stream being captured goes into the graph, where it
+    // changes nothing when replayed); until it has run, pairs alternate
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) return CCE_ERR_CUDA;
+    if (dev >= 0 && dev < kMaxDevices && !g_l2_probed[dev].exchange(true) &&
+        launch_l2_half_probe(device_info().sms, stream) != cudaSuccess)
+      return CCE_ERR_CUDA;
+  }
+  if (record_event(0, 0, stream) != cudaSuccess) return CCE_ERR_CUDA;
+  const cudaError_t le =
+      p.pair ? launch_fwd_lse_pair(tmE, tmC, a, p.grid, g_fwd_stages.load(), stream)
+             : launch_fwd_lse(tmE, tmC, a, p.grid, stream);
+  if (le != cudaSuccess) return CCE_ERR_CUDA;
+  if (record_event(0, 1, stream) != cudaSuccess) return CCE_ERR_CUDA;
+  return CCE_OK;
+}
+
 // shard_stats != nullptr: C is the vocabulary shard starting at global id
 // v_offset; per-token (max, sum exp, target) go to shard_stats [3][N] and
 // loss / lse are not written.
@@ -395,46 +463,10 @@ cce_status_t forward_impl(const void* E, const void* C, const int64_t* y, int64_
   if (ws_bytes < p.ws_bytes) return CCE_ERR_WORKSPACE_TOO_SMALL;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
 
-  CUtensorMap tmE, tmC;
-  if (!make_map(&tmE, E, N, D, BM) || !make_map(&tmC, C, V, D, p.pair ? BM : BN)) return CCE_ERR_CUDA;
-
   unsigned long long* status = reinterpret_cast<unsigned long long*>(ws);
-  float2* partial = reinterpret_cast<float2*>(reinterpret_cast<char*>(ws) + STATUS_BYTES);
   if (cudaMemsetAsync(status, 0, STATUS_BYTES, stream) != cudaSuccess) return CCE_ERR_CUDA;
-
-  FwdArgs a;
-  a.N = (int)N;
-  a.D = (int)D;
-  a.V = (int)V;
-  a.n_mblk = p.n_mblk;
-  a.n_vtile = p.n_vtile;
-  a.n_split = p.n_split;
-  a.n_units = p.n_mblk * p.n_split;
-  a.group_m = p.group_m;
-  a.partial = partial;
-  a.dbg_logits = dbg_logits;
-  a.status = status;
-  a.wait_limit_ns = g_wait_limit_ns.load();
-  a.withhold_loads = g_withhold_loads.load();
-  a.pf = g_fwd_pf.load();
-  a.l2_hints = g_fwd_l2_hints.load();
-  a.sched = p.pair ? g_fwd_order.load() : 0;
-  if (a.sched) {
-    // which L2 half each SM is in: found once per device and process (the
-    // first launch on a stream being captured goes into the graph, where it
-    // changes nothing when replayed); until it has run, pairs alternate
-    int dev = -1;
-    if (cudaGetDevice(&dev) != cudaSuccess) return CCE_ERR_CUDA;
-    if (dev >= 0 && dev < kMaxDevices && !g_l2_probed[dev].exchange(true) &&
-        launch_l2_half_probe(device_info().sms, stream) != cudaSuccess)
-      return CCE_ERR_CUDA;
-  }
-  if (record_event(0, 0, stream) != cudaSuccess) return CCE_ERR_CUDA;
-  const cudaError_t le =
-      p.pair ? launch_fwd_lse_pair(tmE, tmC, a, p.grid, g_fwd_stages.load(), stream)
-             : launch_fwd_lse(tmE, tmC, a, p.grid, stream);
-  if (le != cudaSuccess) return CCE_ERR_CUDA;
-  if (record_event(0, 1, stream) != cudaSuccess) return CCE_ERR_CUDA;
+  const cce_status_t st = launch_logit_pass(E, C, N, D, V, p, ws, dbg_logits, stream);
+  if (st != CCE_OK) return st;
 
   FinArgs f;
   f.N = (int)N;
@@ -442,7 +474,7 @@ cce_status_t forward_impl(const void* E, const void* C, const int64_t* y, int64_
   f.V = (int)V;
   f.n_split = p.n_split;
   f.ignore_index = ignore_index;
-  f.partial = partial;
+  f.partial = reinterpret_cast<const float2*>(reinterpret_cast<char*>(ws) + STATUS_BYTES);
   f.status = status;
   f.shard_stats = shard_stats;
   f.v_offset = v_offset;
@@ -629,7 +661,8 @@ namespace {
 // launch per token super-block; a: the common backward arguments.
 cce_status_t backward_stripes(const void* E, const void* C, void* dE, void* dC, const BwdPlan& bp, const BwdArgs& a,
                               bool accumulate, bool ordered, int sms, char* ws, cudaStream_t stream,
-                              const int* blk_flat = nullptr) {
+                              const int* blk_flat = nullptr, const TargetBuffers* tg = nullptr,
+                              float temperature = 1.f, bool dC_bf16 = false) {
   const StripeLayout& L = bp.stripes;
   void* G = ws + L.off_G;
   CUtensorMap maps[9];
@@ -638,7 +671,7 @@ cce_status_t backward_stripes(const void* E, const void* C, void* dE, void* dC, 
       !make_map(&maps[2], G, Grows, L.Vs, 32) || !make_map(&maps[3], G, Grows, L.Vs, 128) ||
       !make_map(&maps[4], G, Grows, L.Vs, 64) || !make_map(&maps[5], E, a.N, a.D, 64) ||
       !make_map(&maps[6], C, a.V, a.D, 64) || !make_map_f32(&maps[7], dE, a.N, a.D) ||
-      !make_map_f32(&maps[8], dC, a.V, a.D))
+      !(dC_bf16 ? make_map(&maps[8], dC, a.V, a.D, 32) : make_map_f32(&maps[8], dC, a.V, a.D)))
     return CCE_ERR_CUDA;
   unsigned char* ctr = reinterpret_cast<unsigned char*>(ws + L.off_ctr);
   StripeArgs sa{};
@@ -659,6 +692,15 @@ cce_status_t backward_stripes(const void* E, const void* C, void* dE, void* dC, 
   sa.doneC = sa.doneBC + L.n_doneBC;
   sa.nz = a.filter_eps > 0.f ? reinterpret_cast<unsigned char*>(sa.doneC + L.n_doneC) : nullptr;
   sa.blk_flat = blk_flat;
+  if (tg) {
+    sa.tgt_id = tg->id;
+    sa.tgt_w = tg->w;
+    sa.tgt_k = tg->K;
+    sa.row_kind = tg->row_kind;
+    sa.scale2 = LOG2E / temperature;
+    sa.temperature = temperature;
+    sa.dC_bf16 = dC_bf16 ? 1 : 0;
+  }
   sa.ordered = ordered ? 1 : 0;
   sa.status = a.status;
   sa.wait_limit_ns = a.wait_limit_ns;
@@ -969,6 +1011,202 @@ cce_status_t cce_backward_shard(const void* E, const void* C_shard, const int64_
                        dC_shard, workspace, workspace_bytes, stream, true, v_offset);
 }
 
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Distillation from a teacher's top logits
+// ---------------------------------------------------------------------------
+namespace {
+
+constexpr int64_t kMaxTargets = 1024;  // the sort network of distill_targets in shared memory (16 KB)
+
+bool distill_sizes_ok(int64_t N, int64_t D, int64_t V, int64_t K) {
+  // (V: the picking loop compares ids with the end of a 256-column tile in int32)
+  return sizes_ok(N, D, V) && V <= INT_MAX - 2 * BN && K > 0 && K <= kMaxTargets && N * K <= (int64_t)1 << 40;
+}
+
+// Workspace: status | forward: partials, split sums | row kinds | entropies |
+// sorted ids | weights | backward: fp32 sums of bf16 outputs, stripes.
+struct DistillLayout {
+  FwdPlan fwd;        // forward only
+  size_t off_dot, off_kind, off_ent, off_id, off_w, off_dE32, off_dC32, bytes;
+  bool dC_direct;     // backward, bf16 outputs: the dC tiles are stored as bf16 by the stripe kernel
+  StripeLayout stripes;
+};
+
+void plan_targets(int64_t N, int64_t K, size_t at, DistillLayout* L) {
+  L->off_kind = at;
+  L->off_ent = L->off_kind + align_up((size_t)N * 4, 256);
+  L->off_id = L->off_ent + align_up((size_t)N * 4, 256);
+  L->off_w = L->off_id + align_up((size_t)N * K * 4, 256);
+  L->bytes = L->off_w + align_up((size_t)N * K * 4, 256);
+}
+
+bool plan_distill_forward(int64_t N, int64_t D, int64_t V, int64_t K, DistillLayout* L) {
+  if (!distill_sizes_ok(N, D, V, K) || !plan_forward(N, D, V, &L->fwd, true)) return false;
+  L->off_dot = L->fwd.ws_bytes;
+  plan_targets(N, K, L->off_dot + align_up((size_t)L->fwd.n_split * N * 4, 256), L);
+  return true;
+}
+
+constexpr unsigned kDistillFlags = CCE_BWD_DETERMINISTIC | CCE_BWD_BF16_GRADS | CCE_BWD_ACCUMULATE;
+
+bool plan_distill_backward(int64_t N, int64_t D, int64_t V, int64_t K, unsigned flags, DistillLayout* L) {
+  if (!distill_sizes_ok(N, D, V, K) || (flags & ~kDistillFlags)) return false;
+  plan_targets(N, K, STATUS_BYTES, L);
+  const bool bf16 = (flags & CCE_BWD_BF16_GRADS) != 0;
+  // One launch covers every token and nothing is added to: each dC tile is
+  // final when its task ends, and is rounded and stored there (no fp32 copy
+  // of dC, V D 4 bytes, and no pass over it).
+  const int64_t per_launch = 256 * (int64_t)std::max(1, std::min(kStripeMaxM2, g_stripe_m2.load()));
+  L->dC_direct = bf16 && !(flags & CCE_BWD_ACCUMULATE) && N <= per_launch;
+  L->off_dE32 = L->off_dC32 = 0;
+  if (bf16) {
+    L->off_dE32 = L->bytes;
+    L->bytes += align_up((size_t)N * D * 4, 256);
+    if (!L->dC_direct) {
+      L->off_dC32 = L->bytes;
+      L->bytes += align_up((size_t)V * D * 4, 256);
+    }
+  }
+  L->stripes = plan_stripes(N, D, V, L->bytes);
+  L->bytes = L->stripes.bytes;
+  return true;
+}
+
+bool temperature_ok(float t) { return t > 0.f && t <= 3.0e38f && 1.f / t > 0.f && LOG2E / t <= 3.0e38f; }
+
+cce_status_t prepare_targets(const int64_t* ids, const void* teacher, int teacher_dtype, int64_t N, int64_t V,
+                             int64_t K, int64_t ignore_index, float temperature, char* ws, const DistillLayout& L,
+                             TargetBuffers* tg, cudaStream_t stream) {
+  tg->id = reinterpret_cast<int*>(ws + L.off_id);
+  tg->w = reinterpret_cast<float*>(ws + L.off_w);
+  tg->neg_entropy = reinterpret_cast<float*>(ws + L.off_ent);
+  tg->row_kind = reinterpret_cast<int*>(ws + L.off_kind);
+  tg->K = (int)K;
+  TargetArgs t{};
+  t.N = (int)N;
+  t.V = (int)V;
+  t.K = (int)K;
+  t.ignore_index = ignore_index;
+  t.inv_temperature = 1.0 / (double)temperature;
+  t.ids = ids;
+  t.teacher = teacher;
+  t.teacher_bf16 = teacher_dtype == CCE_DTYPE_BF16 ? 1 : 0;
+  t.tgt_id = tg->id;
+  t.tgt_w = tg->w;
+  t.neg_entropy = tg->neg_entropy;
+  t.row_kind = tg->row_kind;
+  t.status = reinterpret_cast<unsigned long long*>(ws);
+  return launch_distill_targets(t, stream) == cudaSuccess ? CCE_OK : CCE_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t cce_distill_forward_workspace_size(int64_t N, int64_t D, int64_t V, int64_t K) {
+  DistillLayout L{};
+  return plan_distill_forward(N, D, V, K, &L) ? L.bytes : 0;
+}
+
+size_t cce_distill_backward_workspace_size(int64_t N, int64_t D, int64_t V, int64_t K, unsigned flags) {
+  DistillLayout L{};
+  return plan_distill_backward(N, D, V, K, flags, &L) ? L.bytes : 0;
+}
+
+cce_status_t cce_distill_forward(const void* E, const void* C, const int64_t* ids, const void* teacher,
+                                 int teacher_dtype, int64_t N, int64_t D, int64_t V, int64_t K, int64_t ignore_index,
+                                 float temperature, float* loss, float* lse, void* workspace, size_t workspace_bytes,
+                                 void* stream_) {
+  if (!E || !C || !ids || !teacher || !loss || !lse || !workspace) return CCE_ERR_INVALID_ARG;
+  if (!distill_sizes_ok(N, D, V, K) || !temperature_ok(temperature)) return CCE_ERR_INVALID_ARG;
+  if (teacher_dtype != CCE_DTYPE_F32 && teacher_dtype != CCE_DTYPE_BF16) return CCE_ERR_INVALID_ARG;
+  if (!aligned(E, 16) || !aligned(C, 16) || !aligned(ids, 8) || !aligned(loss, 4) || !aligned(lse, 4) ||
+      !aligned(teacher, teacher_dtype == CCE_DTYPE_BF16 ? 2 : 4) || !aligned(workspace, 256))
+    return CCE_ERR_MISALIGNED;
+  if (!device_info().ok) return CCE_ERR_UNSUPPORTED_DEVICE;
+  DistillLayout L{};
+  if (!plan_distill_forward(N, D, V, K, &L)) return CCE_ERR_INVALID_ARG;
+  if (workspace_bytes < L.bytes) return CCE_ERR_WORKSPACE_TOO_SMALL;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  char* ws = reinterpret_cast<char*>(workspace);
+  if (cudaMemsetAsync(ws, 0, STATUS_BYTES, stream) != cudaSuccess) return CCE_ERR_CUDA;
+  TargetBuffers tg;
+  cce_status_t st = prepare_targets(ids, teacher, teacher_dtype, N, V, K, ignore_index, temperature, ws, L, &tg, stream);
+  if (st != CCE_OK) return st;
+  float* dot = reinterpret_cast<float*>(ws + L.off_dot);
+  st = launch_logit_pass(E, C, N, D, V, L.fwd, ws, nullptr, stream, &tg, dot, LOG2E / temperature);
+  if (st != CCE_OK) return st;
+  DistillFinArgs f{};
+  f.N = (int)N;
+  f.n_split = L.fwd.n_split;
+  f.temperature = temperature;
+  f.partial = reinterpret_cast<const float2*>(ws + STATUS_BYTES);
+  f.dot = dot;
+  f.neg_entropy = tg.neg_entropy;
+  f.row_kind = tg.row_kind;
+  f.status = reinterpret_cast<const unsigned long long*>(ws);
+  f.loss = loss;
+  f.lse = lse;
+  return launch_distill_finalize(f, stream) == cudaSuccess ? CCE_OK : CCE_ERR_CUDA;
+}
+
+cce_status_t cce_distill_backward(const void* E, const void* C, const int64_t* ids, const void* teacher,
+                                  int teacher_dtype, const float* lse, const float* dloss, int64_t N, int64_t D,
+                                  int64_t V, int64_t K, int64_t ignore_index, float temperature, unsigned flags,
+                                  void* dE, void* dC, void* workspace, size_t workspace_bytes, void* stream_) {
+  if (!E || !C || !ids || !teacher || !lse || !dloss || !dE || !dC || !workspace) return CCE_ERR_INVALID_ARG;
+  if (!distill_sizes_ok(N, D, V, K) || !temperature_ok(temperature)) return CCE_ERR_INVALID_ARG;
+  if (teacher_dtype != CCE_DTYPE_F32 && teacher_dtype != CCE_DTYPE_BF16) return CCE_ERR_INVALID_ARG;
+  if (flags & ~kDistillFlags) return CCE_ERR_INVALID_ARG;
+  if (!aligned(E, 16) || !aligned(C, 16) || !aligned(ids, 8) || !aligned(lse, 4) || !aligned(dloss, 4) ||
+      !aligned(teacher, teacher_dtype == CCE_DTYPE_BF16 ? 2 : 4) || !aligned(dE, 16) || !aligned(dC, 16) ||
+      !aligned(workspace, 256))
+    return CCE_ERR_MISALIGNED;
+  DistillLayout L{};
+  if (!plan_distill_backward(N, D, V, K, flags, &L)) return CCE_ERR_INVALID_ARG;
+  const DeviceInfo di = device_info();
+  if (!di.ok || di.sms < 2) return CCE_ERR_UNSUPPORTED_DEVICE;
+  if (workspace_bytes < L.bytes) return CCE_ERR_WORKSPACE_TOO_SMALL;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  char* ws = reinterpret_cast<char*>(workspace);
+  if (cudaMemsetAsync(ws, 0, STATUS_BYTES, stream) != cudaSuccess) return CCE_ERR_CUDA;
+  TargetBuffers tg;
+  cce_status_t st = prepare_targets(ids, teacher, teacher_dtype, N, V, K, ignore_index, temperature, ws, L, &tg, stream);
+  if (st != CCE_OK) return st;
+
+  const bool bf16 = (flags & CCE_BWD_BF16_GRADS) != 0;
+  const bool accumulate = (flags & CCE_BWD_ACCUMULATE) != 0;
+  // fp32 sums: the outputs themselves, or scratch rounded once at the end
+  float* dE32 = bf16 ? reinterpret_cast<float*>(ws + L.off_dE32) : reinterpret_cast<float*>(dE);
+  void* dC_sum = bf16 && !L.dC_direct ? static_cast<void*>(ws + L.off_dC32) : dC;
+  const bool acc32 = accumulate && !bf16;
+  if (!acc32 && cudaMemsetAsync(dE32, 0, (size_t)N * D * sizeof(float), stream) != cudaSuccess) return CCE_ERR_CUDA;
+  BwdPlan bp{};
+  bp.stripes = L.stripes;
+  BwdArgs a{};
+  a.N = (int)N;
+  a.D = (int)D;
+  a.V = (int)V;
+  a.ignore_index = ignore_index;
+  a.lse = lse;
+  a.dloss = dloss;
+  a.status = reinterpret_cast<unsigned long long*>(ws);
+  a.wait_limit_ns = g_wait_limit_ns.load();
+  a.withhold_loads = g_withhold_loads.load();
+  a.trace = g_bwd_trace.load();
+  a.trace_cap = g_bwd_trace_cap.load();
+  st = backward_stripes(E, C, dE32, dC_sum, bp, a, acc32, (flags & CCE_BWD_DETERMINISTIC) != 0, di.sms, ws, stream,
+                        nullptr, &tg, temperature, L.dC_direct);
+  if (st != CCE_OK || !bf16) return st;
+  if (launch_f32_to_bf16(dE32, dE, (size_t)N * D, accumulate, di.sms, stream) != cudaSuccess) return CCE_ERR_CUDA;
+  if (!L.dC_direct && launch_f32_to_bf16(reinterpret_cast<const float*>(dC_sum), dC, (size_t)V * D, accumulate,
+                                         di.sms, stream) != cudaSuccess)
+    return CCE_ERR_CUDA;
+  return CCE_OK;
+}
+
 cce_status_t cce_read_status(const void* workspace, void* stream, cce_counters_t* out) {
   if (!workspace || !out) return CCE_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -1000,6 +1238,6 @@ const char* cce_status_string(cce_status_t s) {
   return "CCE_ERR_UNKNOWN";
 }
 
-int cce_version(void) { return 103; }
+int cce_version(void) { return 104; }
 
 }  // extern "C"

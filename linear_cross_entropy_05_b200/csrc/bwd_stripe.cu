@@ -99,6 +99,11 @@ __device__ __forceinline__ void stage_f32_block(uint8_t* xb, int lane, const flo
 
 }  // namespace
 
+// PICK (distillation): G = dloss T (softmax(z / T) - targets) with a sorted
+// list of targets per row in the place of one label; dC tiles can be stored
+// as bf16.  Each row finds its first target of the tile by bisection while
+// its accumulator is still being formed.
+template <bool PICK>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SP_THREADS, 1)
     bwd_stripe_kernel(const __grid_constant__ StripeMaps mp, const StripeArgs a, __nv_bfloat16* G) {
   extern __shared__ uint8_t smem_raw[];
@@ -504,6 +509,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SP_THREADS, 1)
       unsigned long long tmask;
       if (!take_task(k, t, tmask, true)) break;
       if (t.type == TASK_END) break;
+      const int* tg_ids = nullptr;
+      const float* tg_w = nullptr;
+      int tg_pos = 0, tg_n = 0, tg_next = INT_MAX;
+      if constexpr (PICK) {
+        const int row = a.tok0 + t.a * 256 + r * 128 + lg * 32 + lane;
+        if (t.type == TASK_A && row < a.N && __ldg(a.row_kind + row) == ROW_LIVE) {
+          tg_ids = a.tgt_id + (size_t)row * a.tgt_k;
+          tg_w = a.tgt_w + (size_t)row * a.tgt_k;
+          tg_n = a.tgt_k;
+          tg_pos = lower_bound_id(tg_ids, tg_n, t.b * BN + hsel * 128);
+          if (tg_pos < tg_n) tg_next = __ldg(tg_ids + tg_pos);
+        }
+      }
       if (!warp_wait(&tfull[acc], acc_phase)) break;
       tc_fence_after();
       if (trace && k < a.trace_cap) trace[k * 4 + 1] = global_timer_ns();
@@ -517,16 +535,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SP_THREADS, 1)
         const int blk_row0 = a.tok0 + t.a * 256 + r * 128;
         const bool blk_is_flat = a.blk_flat != nullptr && blk_row0 < a.N && a.blk_flat[blk_row0 / BM] != 0;
         bool valid = row < a.N && !blk_is_flat;
-        long long yl = valid ? a.y[row] : a.ignore_index;
-        if (yl == a.ignore_index) valid = false;
-        if (a.shard_mode) {
-          yl -= a.v_offset;
-        } else if (valid && (yl < 0 || yl >= a.V)) {
-          valid = false;
-          atomicOr(a.status + ST_FLAGS, SF_BAD_LABEL);
+        long long yl = -1;
+        if constexpr (PICK) {
+          valid = tg_n > 0;
+        } else {
+          yl = valid ? a.y[row] : a.ignore_index;
+          if (yl == a.ignore_index) valid = false;
+          if (a.shard_mode) {
+            yl -= a.v_offset;
+          } else if (valid && (yl < 0 || yl >= a.V)) {
+            valid = false;
+            atomicOr(a.status + ST_FLAGS, SF_BAD_LABEL);
+          }
         }
         const float lse2 = valid ? a.lse[row] * LOG2E : 0.f;
-        const float dl = valid ? a.dloss[row] : 0.f;
+        const float dl = valid ? (PICK ? a.dloss[row] * a.temperature : a.dloss[row]) : 0.f;
         const long long yrel = yl - (long long)t.b * BN;
         const int ycol = (valid && yrel >= 0 && yrel < BN) ? (int)yrel : -1;
         const int ncols = min(BN, a.V - t.b * BN);
@@ -541,8 +564,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SP_THREADS, 1)
           tmem_ld32(tacc + (uint32_t)(c * 32), x);
           uint32_t pk[16];
           bool kept = false;
+          if constexpr (PICK) {
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) {
+            for (int j = 0; j < 32; ++j) x[j] = ex2_approx(fmaf(x[j], a.scale2, -lse2));
+            const int cbase = t.b * BN + c * 32;
+            // (a target that is listed twice is met twice)
+            while (__any_sync(0xffffffffu, tg_next < cbase + 32)) {
+              const int at = tg_next - cbase;
+              const float w = at < 32 ? __ldg(tg_w + tg_pos) : 0.f;
+#pragma unroll
+              for (int j = 0; j < 32; ++j) x[j] -= (j == at) ? w : 0.f;
+              if (at < 32) {
+                ++tg_pos;
+                tg_next = tg_pos < tg_n ? __ldg(tg_ids + tg_pos) : INT_MAX;
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < 32; j += 2)
+              pk[j >> 1] = pack_bf16x2(valid && c * 32 + j < ncols ? dl * x[j] : 0.f,
+                                       valid && c * 32 + j + 1 < ncols ? dl * x[j + 1] : 0.f);
+          }
+#pragma unroll
+          for (int j = 0; j < 32 && !PICK; j += 2) {
             float g2[2];
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
@@ -640,8 +683,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SP_THREADS, 1)
         // no live K block: the accumulator was not written; the tile is zero
         // (stored as zeros by a dC task that writes, skipped by one that adds)
         const bool empty_task = tmask == 0ull;
+        if (PICK && isB && a.dC_bf16) {
+          // the finished dC tile rounded once to bf16, in two boxes of 64 columns
+#pragma unroll 1
+          for (int cc = 0; cc < 4; ++cc) {
+            const int c = hsel * 4 + cc;
+            if (c * 32 >= nd) break;
+            float v[32];
+            tmem_ld32(tacc + (uint32_t)(c * 32), v);
+            uint8_t* rowp = stg + (cc >> 1) * 4096 + lane * 128;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              *reinterpret_cast<uint4*>(rowp + ((((cc & 1) * 4 + q) ^ (lane & 7)) << 4)) =
+                  make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
+                             pack_bf16x2(v[8 * q + 4], v[8 * q + 5]), pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          const int x0 = t.b * 256 + hsel * 128;
+          if (lane == 0 && row0 < a.V && hsel * 128 < nd) {
+            if (x0 < a.D) tma_store_2d(&mp.dC, stg, x0, row0);
+            if (x0 + 64 < a.D) tma_store_2d(&mp.dC, stg + 4096, x0 + 64, row0);
+            bulk_commit_group();
+          }
+        }
 #pragma unroll 1
         for (int cc = 0; cc < 4; ++cc) {
+          if (PICK && isB && a.dC_bf16) break;
           const int c = hsel * 4 + cc;
           if (c * 32 >= nd) break;  // a 128-wide chunk fills only the first half
           if (empty_task && add) break;
@@ -732,9 +800,10 @@ cudaError_t launch_bwd_stripe(const CUtensorMap* maps, const StripeArgs& a, void
   mp.dE = maps[7];
   mp.dC = maps[8];
   const size_t smem = bwd_stripe_smem_bytes();
-  cudaError_t e = cudaFuncSetAttribute(bwd_stripe_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  auto kernel = a.tgt_id ? bwd_stripe_kernel<true> : bwd_stripe_kernel<false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  bwd_stripe_kernel<<<grid, SP_THREADS, smem, stream>>>(mp, a, reinterpret_cast<__nv_bfloat16*>(G));
+  kernel<<<grid, SP_THREADS, smem, stream>>>(mp, a, reinterpret_cast<__nv_bfloat16*>(G));
   return cudaGetLastError();
 }
 

@@ -1,6 +1,7 @@
 // Definitions shared by the CCE kernels and the C-ABI front end.
 #pragma once
 
+#include <climits>
 #include <cstdint>
 
 namespace cce {
@@ -74,6 +75,13 @@ struct FwdArgs {
   // its own half's blocks at run time, and takes the other queue's units when
   // its own runs out or runs more than one vocabulary split ahead.
   int sched;
+  // distillation (pair kernel, PICK): every row's sorted target ids and
+  // weights, and where its sum of weight x logit goes, one value per split
+  const int* tgt_id;   // [N][tgt_k] ascending, absent entries last as INT_MAX
+  const float* tgt_w;  // [N][tgt_k]
+  int tgt_k;
+  float* dot;          // [n_split][N]
+  float scale2;        // log2(e) / temperature: exp(z / T) = 2^(scale2 z)
 };
 
 struct FinArgs {
@@ -87,6 +95,33 @@ struct FinArgs {
   float* shard_stats;
   long long v_offset;
   float* row_max;        // optional [N]: max_v z_iv, the largest logit of each token
+};
+
+// Distillation from a teacher's top logits (distill.cu).
+enum RowKind : int { ROW_EMPTY = 0, ROW_LIVE = 1, ROW_BAD = 2 };
+struct TargetArgs {
+  int N, V, K;
+  long long ignore_index;
+  double inv_temperature;
+  const int64_t* ids;   // [N][K]
+  const void* teacher;  // [N][K] fp32 or bf16
+  int teacher_bf16;
+  int* tgt_id;          // [N][K] out: ids in ascending order, INT_MAX past the last
+  float* tgt_w;         // [N][K] out: the teacher's probabilities in that order
+  float* neg_entropy;   // [N] out: sum_k p_k log p_k
+  int* row_kind;        // [N] out: RowKind
+  unsigned long long* status;
+};
+struct DistillFinArgs {
+  int N, n_split;
+  float temperature;
+  const float2* partial;     // [n_split][N]
+  const float* dot;          // [n_split][N]
+  const float* neg_entropy;  // [N]
+  const int* row_kind;       // [N]
+  const unsigned long long* status;
+  float* loss;
+  float* lse;
 };
 
 struct PrepArgs {
@@ -356,7 +391,29 @@ struct StripeArgs {
   // block (its label entries go to the flat-row kernel; its rows of G are
   // zero, and a recompute task whose two blocks are both flat is skipped)
   const int* blk_flat;
+  // distillation: sorted targets of every row (as in FwdArgs) in the place of
+  // y; rows whose kind is not ROW_LIVE have no gradient
+  const int* tgt_id;
+  const float* tgt_w;
+  int tgt_k;
+  const int* row_kind;
+  float scale2;          // log2(e) / temperature
+  float temperature;     // G = dloss * temperature * (softmax - targets)
+  int dC_bf16;           // 1: dC-tile tasks store bf16 (dC_add = 0; the dC map is of bf16 boxes)
 };
+
+// First position of the ascending ids[0 .. n) that is not below `first`.
+__device__ __forceinline__ int lower_bound_id(const int* __restrict__ ids, int n, int first) {
+  int lo = 0, hi = n;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(ids + mid) < first)
+      lo = mid + 1;
+    else
+      hi = mid;
+  }
+  return lo;
+}
 
 // Fixed-point exponent s: contributions are stored as round(x * 2^s) in int64.
 // Every gradient entry is bounded by

@@ -1,0 +1,190 @@
+// Distillation from a teacher's top logits: the two small kernels around the
+// logit pass (fwd.cu, PICK) and the stripe backward (bwd_stripe.cu, PICK).
+//
+// For a token with teacher entries (id_k, t_k), k < K, and a temperature T:
+//   p_k    = exp(t_k / T) / sum_j exp(t_j / T)   over the row's live entries
+//   lse    = log sum_v exp(z_v / T),   z_v = E_i . C_v
+//   loss   = T^2 sum_k p_k (log p_k - z_{id_k} / T + lse)
+//   dloss / dz_v = T (exp(z_v / T - lse) - sum_{k: id_k = v} p_k)
+// An entry is live unless its id is ignore_index or its logit -inf.  The
+// teacher's side costs N K (8 + 4) bytes, nothing beside the logit pass; it
+// is kept in double (sums and exponentials) and rounded once to float.
+//
+// distill_targets  one block per row: p, sum p log p, and the entries sorted
+//                  by id, so that the logit and gradient tiles, which walk
+//                  the vocabulary in order, meet them one after another.
+// distill_finalize merges the splits' (max, sum, weighted logits) into lse
+//                  and loss; 32 rows x 8 split lanes per block, so the
+//                  [split][row] partials are read in whole lines.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+
+namespace cce {
+
+namespace {
+
+// Reduction of one double per thread over the block (at most 256 threads,
+// whole warps), in a fixed order; every thread gets the result.
+template <bool MAX>
+__device__ __forceinline__ double block_reduce(double v, double* buf) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const double u = __shfl_xor_sync(0xffffffffu, v, o);
+    v = MAX ? fmax(v, u) : v + u;
+  }
+  __syncthreads();  // buf may still be read from an earlier reduction
+  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
+  __syncthreads();
+  double r = buf[0];
+  for (int i = 1; i < (int)(blockDim.x >> 5); ++i) r = MAX ? fmax(r, buf[i]) : r + buf[i];
+  return r;
+}
+
+}  // namespace
+
+// n_sort: K rounded up to a power of two (the sort network's size)
+__global__ void __launch_bounds__(256) distill_targets_kernel(const TargetArgs a, int n_sort) {
+  extern __shared__ double smem_d[];
+  double* sx = smem_d;                                                     // [K] t / T, -inf if not live
+  unsigned long long* key = reinterpret_cast<unsigned long long*>(sx + a.K);  // [n_sort] id << 32 | position
+  double* buf = reinterpret_cast<double*>(key + n_sort);                   // [8]
+  const int row = blockIdx.x;
+  const size_t base = (size_t)row * a.K;
+  const int tid = threadIdx.x;
+
+  int bad = 0;
+  double top = -INFINITY;
+  for (int k = tid; k < n_sort; k += blockDim.x) {
+    unsigned id = INT_MAX;
+    if (k < a.K) {
+      const long long raw = a.ids[base + k];
+      const float t = a.teacher_bf16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(a.teacher)[base + k])
+                                     : reinterpret_cast<const float*>(a.teacher)[base + k];
+      double x = -INFINITY;
+      if (raw != a.ignore_index && t != -INFINITY) {
+        if (raw < 0 || raw >= a.V || !(t < INFINITY)) {
+          bad = 1;  // an id outside the vocabulary, a NaN or +inf logit
+        } else {
+          id = (unsigned)raw;
+          x = (double)t * a.inv_temperature;
+        }
+      }
+      sx[k] = x;
+      top = fmax(top, x);
+    }
+    key[k] = ((unsigned long long)id << 32) | (unsigned)k;
+  }
+  bad = __syncthreads_or(bad);
+  top = block_reduce<true>(top, buf);
+  const int kind = bad ? ROW_BAD : (top == -INFINITY ? ROW_EMPTY : ROW_LIVE);
+  if (tid == 0) {
+    a.row_kind[row] = kind;
+    if (bad) atomicOr(a.status + ST_FLAGS, SF_BAD_LABEL);
+    if (kind != ROW_LIVE) a.neg_entropy[row] = 0.f;
+  }
+  if (kind != ROW_LIVE) {
+    for (int k = tid; k < a.K; k += blockDim.x) {
+      a.tgt_id[base + k] = INT_MAX;
+      a.tgt_w[base + k] = 0.f;
+    }
+    return;
+  }
+
+  double s = 0.0, sxw = 0.0;  // sum of exp(x - top) and of exp(x - top) (x - top)
+  for (int k = tid; k < a.K; k += blockDim.x) {
+    const double d = sx[k] - top;
+    const double e = exp(d);
+    s += e;
+    if (e > 0.0) sxw += e * d;
+  }
+  s = block_reduce<false>(s, buf);
+  sxw = block_reduce<false>(sxw, buf);
+  if (tid == 0) a.neg_entropy[row] = (float)(sxw / s - log(s));
+
+  // bitonic sort by id (then position)
+  for (int size = 2; size <= n_sort; size <<= 1) {
+    for (int stride = size >> 1; stride > 0; stride >>= 1) {
+      __syncthreads();
+      for (int i = tid; i < (n_sort >> 1); i += blockDim.x) {
+        const int lo = 2 * i - (i & (stride - 1));
+        const int hi = lo + stride;
+        const bool up = (lo & size) == 0;
+        const unsigned long long ka = key[lo], kb = key[hi];
+        if ((ka > kb) == up) {
+          key[lo] = kb;
+          key[hi] = ka;
+        }
+      }
+    }
+  }
+  __syncthreads();
+  const double inv = 1.0 / s;
+  for (int k = tid; k < a.K; k += blockDim.x) {
+    const unsigned long long kk = key[k];
+    const double x = sx[(unsigned)kk & 0xffffu];
+    a.tgt_id[base + k] = (int)(kk >> 32);
+    a.tgt_w[base + k] = x == -INFINITY ? 0.f : (float)(exp(x - top) * inv);
+  }
+}
+
+__global__ void __launch_bounds__(256) distill_finalize_kernel(const DistillFinArgs a) {
+  __shared__ float sm[8][32];
+  __shared__ float ss[8][32];
+  __shared__ double sd[8][32];
+  const int lane = threadIdx.x, part = threadIdx.y;
+  const int row = blockIdx.x * 32 + lane;
+  const float scale2 = LOG2E / a.temperature;
+  float M = -INFINITY, s = 0.f;
+  double dot = 0.0;
+  if (row < a.N) {
+    for (int r = part; r < a.n_split; r += 8) {
+      const float2 p = a.partial[(size_t)r * a.N + row];
+      dot += (double)a.dot[(size_t)r * a.N + row];
+      const float m = fmaxf(M, p.x);
+      if (m != -INFINITY) s = s * exp2f((M - m) * scale2) + p.y * exp2f((p.x - m) * scale2);
+      M = m;
+    }
+  }
+  sm[part][lane] = M;
+  ss[part][lane] = s;
+  sd[part][lane] = dot;
+  __syncthreads();
+  if (part != 0 || row >= a.N) return;
+  for (int q = 1; q < 8; ++q) M = fmaxf(M, sm[q][lane]);
+  s = 0.f;
+  dot = 0.0;
+  for (int q = 0; q < 8; ++q) {
+    if (sm[q][lane] != -INFINITY) s += ss[q][lane] * exp2f((sm[q][lane] - M) * scale2);
+    dot += sd[q][lane];
+  }
+  const double T = (double)a.temperature;
+  const double L = (double)M / T + log((double)s);
+  const int kind = a.row_kind[row];
+  double loss = 0.0;
+  if (kind == ROW_LIVE)
+    loss = T * T * ((double)a.neg_entropy[row] - dot / T + L);
+  float lse = (float)L, out = (float)loss;
+  if (kind == ROW_BAD) out = __int_as_float(0x7fc00000);
+  // a bounded wait gave up: some partials may be an earlier call's
+  if (a.status[ST_FLAGS] & SF_TIMEOUT) lse = out = __int_as_float(0x7fc00000);
+  a.lse[row] = lse;
+  a.loss[row] = out;
+}
+
+cudaError_t launch_distill_targets(const TargetArgs& a, cudaStream_t stream) {
+  int n_sort = 32;
+  while (n_sort < a.K) n_sort <<= 1;
+  const int threads = n_sort / 2 < 32 ? 32 : (n_sort / 2 > 256 ? 256 : n_sort / 2);
+  const size_t smem = (size_t)a.K * 8 + (size_t)n_sort * 8 + 64;
+  distill_targets_kernel<<<a.N, threads, smem, stream>>>(a, n_sort);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_distill_finalize(const DistillFinArgs& a, cudaStream_t stream) {
+  distill_finalize_kernel<<<(a.N + 31) / 32, dim3(32, 8), 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace cce

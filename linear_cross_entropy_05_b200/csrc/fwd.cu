@@ -38,9 +38,26 @@ namespace cce {
 // Fold one 128 x 256 logit tile held in TMEM (this thread's lane = one token
 // row) into the row's running (max, sum exp(z - max)).  Columns >= V are
 // masked to -inf; DUMP additionally stores the raw logits (debug entry only).
-template <bool DUMP>
+//
+// PICK (distillation): the row's targets are met in ascending order as the
+// tiles pass, so their logits are taken from the accumulator they are in and
+// no gather of C rows is needed.  The picking loop is entered by the whole
+// warp when any of its rows has a target in the 32 columns (K = 64 targets
+// over 256000 columns: one chunk in four), and one select per column finds
+// the value, since registers cannot be indexed.
+struct RowTargets {
+  const int* ids;
+  const float* w;
+  int pos, n;
+  int next;    // id of the next target, INT_MAX after the last
+  float dot;   // sum of weight x logit so far
+  __device__ __forceinline__ void load() { next = pos < n ? __ldg(ids + pos) : INT_MAX; }
+};
+
+template <bool DUMP, bool PICK>
 __device__ __forceinline__ void lse_fold_tile(uint32_t tbase, int col0, int row, const FwdArgs& a, float& mrun,
-                                              float& srun) {
+                                              float& srun, RowTargets& tg) {
+  const float scale2 = PICK ? a.scale2 : LOG2E;
 #pragma unroll 1
   for (int c = 0; c < BN / 32; ++c) {
     const int cbase = col0 + c * 32;
@@ -52,6 +69,19 @@ __device__ __forceinline__ void lse_fold_tile(uint32_t tbase, int col0, int row,
         float* dst = a.dbg_logits + (size_t)row * ((size_t)a.n_vtile * BN) + cbase;
 #pragma unroll
         for (int j = 0; j < 32; ++j) dst[j] = x[j];
+      }
+    }
+    if constexpr (PICK) {
+      while (__any_sync(0xffffffffu, tg.next < cbase + 32)) {
+        const int at = tg.next - cbase;
+        float z = 0.f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) z = (j == at) ? x[j] : z;
+        if (at < 32) {
+          tg.dot = fmaf(__ldg(tg.w + tg.pos), z, tg.dot);
+          ++tg.pos;
+          tg.load();
+        }
       }
     }
     const int nvalid = a.V - cbase;
@@ -67,16 +97,16 @@ __device__ __forceinline__ void lse_fold_tile(uint32_t tbase, int col0, int row,
       cm1 = fmaxf(cm1, x[j + 1]);
     }
     const float mnew = fmaxf(mrun, fmaxf(cm0, cm1));
-    const float ms = mnew * LOG2E;
+    const float ms = mnew * scale2;
     float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll
     for (int j = 0; j < 32; j += 4) {
-      s0 += ex2_approx(fmaf(x[j], LOG2E, -ms));
-      s1 += ex2_approx(fmaf(x[j + 1], LOG2E, -ms));
-      s2 += ex2_approx(fmaf(x[j + 2], LOG2E, -ms));
-      s3 += ex2_approx(fmaf(x[j + 3], LOG2E, -ms));
+      s0 += ex2_approx(fmaf(x[j], scale2, -ms));
+      s1 += ex2_approx(fmaf(x[j + 1], scale2, -ms));
+      s2 += ex2_approx(fmaf(x[j + 2], scale2, -ms));
+      s3 += ex2_approx(fmaf(x[j + 3], scale2, -ms));
     }
-    srun = srun * ex2_approx(fmaf(mrun, LOG2E, -ms)) + ((s0 + s1) + (s2 + s3));
+    srun = srun * ex2_approx(fmaf(mrun, scale2, -ms)) + ((s0 + s1) + (s2 + s3));
     mrun = mnew;
   }
 }
@@ -233,6 +263,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       int v0, v1;
       split_range(r, a.n_vtile, a.n_split, v0, v1);
       float mrun = -INFINITY, srun = 0.f;
+      RowTargets none{};
       bool ok = true;
       for (int vt = v0; vt < v1; ++vt) {
         if (!mbar_wait(&tfull[acc], acc_phase, wc)) {
@@ -240,8 +271,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           break;
         }
         tc_fence_after();
-        lse_fold_tile<DUMP>(tmem_base + lane_addr + (uint32_t)(acc * BN), vt * BN, m * BM + row_in_blk, a, mrun,
-                            srun);
+        lse_fold_tile<DUMP, false>(tmem_base + lane_addr + (uint32_t)(acc * BN), vt * BN, m * BM + row_in_blk, a,
+                                   mrun, srun, none);
         tc_fence_before();
         mbar_arrive(&tempty[acc]);
         if (++acc == 2) {
@@ -347,7 +378,7 @@ cudaError_t read_l2_halves(unsigned* out, int n) {
 // arrive on both CTAs' barriers, and both epilogues release the accumulator
 // on the leader's barrier.  No TMA multicast is used.
 // ----------------------------------------------------------------------------
-template <bool DUMP, int S>
+template <bool DUMP, int S, bool PICK>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     fwd_lse_pair_kernel(const __grid_constant__ CUtensorMap tmE, const __grid_constant__ CUtensorMap tmCh,
                         const FwdArgs a) {
@@ -661,14 +692,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       split_range(r, a.n_vtile, a.n_split, v0, v1);
       const int row = m2 * (2 * BM) + (int)rank * BM + row_in_blk;
       float mrun = -INFINITY, srun = 0.f;
+      RowTargets tg{};
+      if constexpr (PICK) {
+        // the row's first target in this split's columns
+        tg.ids = a.tgt_id + (size_t)row * a.tgt_k;
+        tg.w = a.tgt_w + (size_t)row * a.tgt_k;
+        tg.n = row < a.N ? a.tgt_k : 0;
+        tg.pos = lower_bound_id(tg.ids, tg.n, v0 * BN);
+        tg.load();
+      }
       bool ok = true;
       for (int vt = v0; vt < v1; ++vt) {
-        if (!mbar_wait(&tfull[acc], acc_phase, wc)) {
+        bool ready = mbar_wait(&tfull[acc], acc_phase, wc);
+        if constexpr (PICK) ready = __all_sync(0xffffffffu, ready);  // the picking loop needs all lanes
+        if (!ready) {
           ok = false;
           break;
         }
         tc_fence_after();
-        lse_fold_tile<DUMP>(tmem_base + lane_addr + (uint32_t)(acc * BN), vt * BN, row, a, mrun, srun);
+        lse_fold_tile<DUMP, PICK>(tmem_base + lane_addr + (uint32_t)(acc * BN), vt * BN, row, a, mrun, srun, tg);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(acc ? tempty_leader1 : tempty_leader0);
@@ -678,7 +720,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         }
       }
       if (!ok) break;
-      if (row < a.N) a.partial[(size_t)r * a.N + row] = make_float2(mrun, srun);
+      if (row < a.N) {
+        a.partial[(size_t)r * a.N + row] = make_float2(mrun, srun);
+        if constexpr (PICK) a.dot[(size_t)r * a.N + row] = tg.dot;
+      }
     }
   }
 
@@ -853,27 +898,29 @@ size_t fwd_smem_bytes() { return 1024 + (size_t)FWD_STAGES * STAGE_BYTES + 256; 
 size_t fwd_pair_smem_bytes(int stages) { return 1024 + (size_t)stages * PAIR_STAGE_BYTES + 256; }
 
 namespace {
-template <bool DUMP, int S>
+template <bool DUMP, int S, bool PICK>
 cudaError_t launch_pair_stages(const CUtensorMap& tmE, const CUtensorMap& tmCh, const FwdArgs& a, int grid,
                                cudaStream_t stream) {
   const size_t smem = fwd_pair_smem_bytes(S);
-  cudaError_t e = cudaFuncSetAttribute(fwd_lse_pair_kernel<DUMP, S>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
+  cudaError_t e = cudaFuncSetAttribute(fwd_lse_pair_kernel<DUMP, S, PICK>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  fwd_lse_pair_kernel<DUMP, S><<<grid, NUM_THREADS, smem, stream>>>(tmE, tmCh, a);
+  fwd_lse_pair_kernel<DUMP, S, PICK><<<grid, NUM_THREADS, smem, stream>>>(tmE, tmCh, a);
   return cudaGetLastError();
 }
 }  // namespace
 
 // grid: an even number of CTAs (pairs); stages: PAIR_STAGES or PAIR_STAGES_MAX
-// operand stages per CTA (the latter fills the 227 KB of shared memory)
+// operand stages per CTA (the latter fills the 227 KB of shared memory; with
+// targets to pick always the latter)
 cudaError_t launch_fwd_lse_pair(const CUtensorMap& tmE, const CUtensorMap& tmCh, const FwdArgs& a, int grid,
                                 int stages, cudaStream_t stream) {
+  if (a.tgt_id) return launch_pair_stages<false, PAIR_STAGES_MAX, true>(tmE, tmCh, a, grid, stream);
   if (stages == PAIR_STAGES_MAX)
-    return a.dbg_logits ? launch_pair_stages<true, PAIR_STAGES_MAX>(tmE, tmCh, a, grid, stream)
-                        : launch_pair_stages<false, PAIR_STAGES_MAX>(tmE, tmCh, a, grid, stream);
-  return a.dbg_logits ? launch_pair_stages<true, PAIR_STAGES>(tmE, tmCh, a, grid, stream)
-                      : launch_pair_stages<false, PAIR_STAGES>(tmE, tmCh, a, grid, stream);
+    return a.dbg_logits ? launch_pair_stages<true, PAIR_STAGES_MAX, false>(tmE, tmCh, a, grid, stream)
+                        : launch_pair_stages<false, PAIR_STAGES_MAX, false>(tmE, tmCh, a, grid, stream);
+  return a.dbg_logits ? launch_pair_stages<true, PAIR_STAGES, false>(tmE, tmCh, a, grid, stream)
+                      : launch_pair_stages<false, PAIR_STAGES, false>(tmE, tmCh, a, grid, stream);
 }
 
 cudaError_t launch_fwd_lse(const CUtensorMap& tmE, const CUtensorMap& tmC, const FwdArgs& a, int grid,

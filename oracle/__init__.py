@@ -316,3 +316,46 @@ def tile_live_map(E_bits, C_bits, y, lse, ignore_index: int, filter_eps: float,
         _, Dm, _ = softmax_grad_f64(z, lse[r0:r1], y[r0:r1], ones[r0:r1], ignore_index)
         out.append(tile_live_map_f64(Dm, r0, Bn, Bv, filter_eps))
     return np.concatenate(out, axis=0)
+
+
+# ---------------------------------------------------------------------------
+# distillation from a teacher's top logits
+# ---------------------------------------------------------------------------
+
+def distill_targets(ids, teacher, temperature=1.0, ignore_index=-100):
+    """The teacher's distribution p [N, K] (fp64) over each row's live entries
+    (0 elsewhere) and which rows have one.  An entry is live unless its id is
+    ignore_index or its logit -inf."""
+    t = np.asarray(teacher, dtype=np.float64)
+    ids = np.asarray(ids)
+    live = (ids != ignore_index) & ~(t == -np.inf)
+    x = np.where(live, t / temperature, -np.inf)
+    has = live.any(axis=1)
+    top = np.where(has, x.max(axis=1), 0.0)
+    w = np.exp(x - top[:, None])
+    s = w.sum(axis=1)
+    p = w / np.where(has, s, 1.0)[:, None]
+    return p, has
+
+
+def distill(E, C, ids, teacher, temperature=1.0, ignore_index=-100, dloss=None):
+    """loss [N] and lse [N] (fp64) of loss_i = T^2 KL(p_i || softmax(E_i C^T / T))
+    over the teacher's entries; with dloss also dE, dC of sum_i dloss_i loss_i
+    and G.  E, C: fp64 arrays."""
+    T = float(temperature)
+    x = (E @ C.T) / T
+    top = x.max(axis=1)
+    lse = top + np.log(np.exp(x - top[:, None]).sum(axis=1))
+    p, has = distill_targets(ids, teacher, T, ignore_index)
+    rows = np.arange(E.shape[0])[:, None]
+    at = np.where(p > 0, ids, 0)
+    with np.errstate(divide="ignore", invalid="ignore"):
+        plogp = np.where(p > 0, p * np.log(p), 0.0)
+    loss = T * T * (plogp - p * x[rows, at] + p * lse[:, None]).sum(axis=1)
+    loss = np.where(has, loss, 0.0)
+    if dloss is None:
+        return loss, lse
+    target = np.zeros_like(x)
+    np.add.at(target, (np.broadcast_to(rows, at.shape), at), p)
+    G = (np.exp(x - lse[:, None]) - target) * (T * np.asarray(dloss, dtype=np.float64) * has)[:, None]
+    return loss, lse, G @ C, G.T @ E, G
