@@ -55,12 +55,15 @@ typedef enum {
   CCE_ERR_UNSUPPORTED_DEVICE = 4, /* the current device is not sm_100 */
   CCE_ERR_CUDA = 5,               /* a CUDA runtime/driver call failed */
   CCE_ERR_TIMEOUT = 6,            /* device: a bounded wait gave up (cce_read_status) */
-  CCE_ERR_BAD_LABEL = 7           /* device: a label outside [0, V) (cce_read_status) */
+  CCE_ERR_BAD_LABEL = 7,          /* device: a label outside [0, V) (cce_read_status) */
+  CCE_ERR_NONFINITE = 8           /* device: cce_top_logits or cce_sample met a row whose largest
+                                     logit is infinite or NaN (cce_read_status) */
 } cce_status_t;
 
 /* Status block decoded by cce_read_status. */
 typedef struct {
-  uint64_t flags;       /* bit 0: a wait timed out; bit 1: an invalid label was seen */
+  uint64_t flags;       /* bit 0: a wait timed out; bit 1: an invalid label was seen;
+                           bit 2: a row's largest logit is infinite or NaN */
   uint64_t live_tiles;  /* backward: 32x32 units (tokens x vocabulary rows) holding at
                            least one gradient entry that was added */
   uint64_t dead_tiles;  /* backward: units recomputed and found to hold no entry
@@ -362,6 +365,56 @@ CCE_API cce_status_t cce_distill_backward(const void* E, const void* C, const in
                                           int64_t D, int64_t V, int64_t K, int64_t ignore_index, float temperature,
                                           unsigned flags, void* dE, void* dC, void* workspace,
                                           size_t workspace_bytes, void* stream);
+
+/* ---- Choosing among the head's logits ----
+ * z_iv = E_i . C_v for 256 tokens at a time; nothing of size N x V is kept.
+ * -0 counts as +0; among equal logits the lowest id comes first.  A row whose
+ * largest logit is infinite or NaN gets ids of -1 and NaN values, and sets
+ * status flag bit 2; after a bounded wait that gave up (bit 0) every row of
+ * the affected chunk does. */
+
+/* Workspace bytes of cce_top_logits and cce_sample (0 if the sizes are
+ * invalid): the logits of min(N, 256) tokens in fp32 (262 MB at 256 tokens and
+ * 256000 entries), 12 bytes per token and 32 vocabulary entries, and the
+ * status block. */
+CCE_API size_t cce_head_workspace_size(int64_t N, int64_t D, int64_t V);
+
+/* The k largest logits of every token in falling order (values [N x k] fp32,
+ * ids [N x k] int64) and lse [N] fp32 = log sum_v exp(z_iv): what
+ * cce_distill_forward takes of a teacher.  1 <= k <= min(V, 1024). */
+CCE_API cce_status_t cce_top_logits(const void* E, const void* C, int64_t N, int64_t D, int64_t V, int64_t k,
+                                    float* values, int64_t* ids, float* lse, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/* Settings of cce_sample: device arrays [N], or, where the pointer is null,
+ * the *_all value for every row. */
+typedef struct {
+  const float* temperature; /* > 0, or 0: the largest logit (u and the filters do not matter) */
+  const int32_t* top_k;     /* the k largest stay; 0 (or >= V): off */
+  const float* top_p;       /* the shortest prefix, in falling order, of at least this share of the
+                               mass that top_k left (at least one entry); >= 1: off */
+  const float* min_p;       /* entries below this share of the largest one's probability go; 0: off */
+  float temperature_all;
+  int32_t top_k_all;
+  float top_p_all;
+  float min_p_all;
+} cce_sample_settings_t;
+
+/* Draws one token per row: with x = z / temperature, the filters are applied
+ * in the order top_k, top_p, min_p; the token is the first id, in the order of
+ * ids, whose cumulated kept exp(x) is above u times their sum.  The sums are
+ * formed in double.
+ *   u     [N] fp32       a random number in [0, 1) per row
+ *   token [N] int64 out  the id (-1: see above)
+ *   logp  [N] fp32 out   x_token - log sum_v exp(x_v), over all of V, before
+ *                        the filters (at temperature 1 for rows with
+ *                        temperature 0): minus cce_forward's loss of that
+ *                        token at temperature 1
+ * Values of the per-row arrays outside their range act as the nearest inside
+ * it, and NaN as "off" (temperature and u: as 0). */
+CCE_API cce_status_t cce_sample(const void* E, const void* C, int64_t N, int64_t D, int64_t V, const float* u,
+                                const cce_sample_settings_t* settings, int64_t* token, float* logp,
+                                void* workspace, size_t workspace_bytes, void* stream);
 
 /* Synchronises `stream`, then copies the status block of `workspace` (as left
  * by the last call that used it) into *out.  Returns CCE_ERR_TIMEOUT or

@@ -17,7 +17,9 @@ autograd.
 
 On the same head, also without N x V logits in memory: distill_forward,
 distill_backward and linear_distillation (the loss on a teacher's top logits
-and its gradients; cce_distill_forward, cce_distill_backward).
+and its gradients; cce_distill_forward, cce_distill_backward), top_logits (the
+k largest logits per token; cce_top_logits) and sample (one drawn token per
+row; cce_sample).
 """
 from __future__ import annotations
 
@@ -35,6 +37,7 @@ from ._native import (CCE_BWD_ACCUMULATE, CCE_BWD_BF16_GRADS, CCE_BWD_DETERMINIS
                       cce_backward_shard, cce_backward_workspace_size, cce_backward_workspace_size_ex,
                       CCE_DTYPE_BF16, CCE_DTYPE_F32, cce_distill_backward, cce_distill_backward_workspace_size,
                       cce_distill_forward, cce_distill_forward_workspace_size,
+                      CCESampleSettings, cce_head_workspace_size, cce_sample, cce_top_logits,
                       cce_forward_shard, cce_merge_shards, cce_debug_forward_logits,
                       cce_debug_set_backward_trace, cce_debug_set_backward_variant, cce_debug_set_prefetch, cce_debug_set_forward_variant, cce_debug_set_kernel_events, cce_debug_set_wait_limit_ns,
                       cce_debug_withhold_loads, cce_forward, cce_forward_noalloc,
@@ -63,6 +66,7 @@ __all__ = [
     "CCE_DTYPE_F32", "CCE_DTYPE_BF16", "cce_distill_forward", "cce_distill_backward",
     "cce_distill_forward_workspace_size", "cce_distill_backward_workspace_size",
     "distill_forward", "distill_backward", "linear_distillation",
+    "CCESampleSettings", "cce_head_workspace_size", "cce_top_logits", "cce_sample", "top_logits", "sample",
 ]
 
 
@@ -242,6 +246,9 @@ def __getattr__(name):
     if name in ("distill_forward", "distill_backward"):
         from . import _distill
         return getattr(_distill, name)
+    if name in ("top_logits", "sample"):
+        from . import _choose
+        return getattr(_choose, name)
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 

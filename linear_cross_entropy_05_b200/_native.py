@@ -23,6 +23,12 @@ class CCECounters(ctypes.Structure):
                 ("pruned_tiles", ctypes.c_uint64), ("flat_units", ctypes.c_uint64)]
 
 
+class CCESampleSettings(ctypes.Structure):
+    _fields_ = [("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p), ("top_p", ctypes.c_void_p),
+                ("min_p", ctypes.c_void_p), ("temperature_all", ctypes.c_float), ("top_k_all", ctypes.c_int32),
+                ("top_p_all", ctypes.c_float), ("min_p_all", ctypes.c_float)]
+
+
 class CCEError(RuntimeError):
     def __init__(self, status: int, msg: str):
         super().__init__(f"{msg} (status {status})")
@@ -79,6 +85,13 @@ def load_library():
         lib.cce_distill_backward.argtypes = [c_vp, c_vp, c_vp, c_vp, ctypes.c_int, c_vp, c_vp, c_i64, c_i64, c_i64,
                                              c_i64, c_i64, c_f32, ctypes.c_uint, c_vp, c_vp, c_vp, c_size, c_vp]
         lib.cce_distill_backward.restype = ctypes.c_int
+        lib.cce_head_workspace_size.argtypes = [c_i64] * 3
+        lib.cce_head_workspace_size.restype = c_size
+        lib.cce_top_logits.argtypes = [c_vp, c_vp, c_i64, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp, c_size, c_vp]
+        lib.cce_top_logits.restype = ctypes.c_int
+        lib.cce_sample.argtypes = [c_vp, c_vp, c_i64, c_i64, c_i64, c_vp, ctypes.POINTER(CCESampleSettings), c_vp,
+                                   c_vp, c_vp, c_size, c_vp]
+        lib.cce_sample.restype = ctypes.c_int
         lib.cce_read_status.argtypes = [c_vp, c_vp, ctypes.POINTER(CCECounters)]
         lib.cce_read_status.restype = ctypes.c_int
         lib.cce_status_string.argtypes = [ctypes.c_int]
@@ -281,6 +294,27 @@ def cce_distill_backward(E: int, C: int, ids: int, teacher: int, teacher_dtype: 
                                              temperature, flags, dE, dC, workspace, workspace_bytes, stream)
     if check:
         _check(st, "cce_distill_backward")
+    return st
+
+
+def cce_head_workspace_size(N: int, D: int, V: int) -> int:
+    return int(load_library().cce_head_workspace_size(N, D, V))
+
+
+def cce_top_logits(E: int, C: int, N: int, D: int, V: int, k: int, values: int, ids: int, lse: int, workspace: int,
+                   workspace_bytes: int, stream: int, check: bool = True) -> int:
+    st = load_library().cce_top_logits(E, C, N, D, V, k, values, ids, lse, workspace, workspace_bytes, stream)
+    if check:
+        _check(st, "cce_top_logits")
+    return st
+
+
+def cce_sample(E: int, C: int, N: int, D: int, V: int, u: int, settings: CCESampleSettings, token: int, logp: int,
+               workspace: int, workspace_bytes: int, stream: int, check: bool = True) -> int:
+    st = load_library().cce_sample(E, C, N, D, V, u, ctypes.byref(settings), token, logp, workspace,
+                                   workspace_bytes, stream)
+    if check:
+        _check(st, "cce_sample")
     return st
 
 

@@ -47,6 +47,10 @@ cudaError_t launch_flat_rows(const void* E, const void* C, const int64_t* y, con
 cudaError_t launch_f32_to_bf16(const float* src, void* dst, size_t n, bool accumulate, int sms, cudaStream_t stream);
 cudaError_t launch_distill_targets(const TargetArgs& a, cudaStream_t stream);
 cudaError_t launch_distill_finalize(const DistillFinArgs& a, cudaStream_t stream);
+int head_logits_stages(int nt);
+cudaError_t launch_head_logits(const CUtensorMap& tmC, const CUtensorMap& tmE, const HeadArgs& a, int grid,
+                               cudaStream_t stream);
+cudaError_t launch_head_select(const HeadArgs& a, cudaStream_t stream);
 }  // namespace cce
 
 using namespace cce;
@@ -1207,6 +1211,136 @@ cce_status_t cce_distill_backward(const void* E, const void* C, const int64_t* i
   return CCE_OK;
 }
 
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Choosing among the head's logits
+// ---------------------------------------------------------------------------
+namespace {
+
+constexpr int64_t kMaxTop = 1024;
+
+bool head_sizes_ok(int64_t N, int64_t D, int64_t V) {
+  // (V: the last tile's vocabulary index must fit int32)
+  return sizes_ok(N, D, V) && V <= INT_MAX - 2 * BN;
+}
+
+// Workspace: status | a chunk's logits [rows][ld] fp32 | group sums [n_grp][nt]
+// fp64 | group maxima [n_grp][nt] fp32.
+struct HeadLayout {
+  int rows, nt, n_grp, ld;
+  size_t off_logits, off_mass, off_max, bytes;
+};
+
+HeadLayout plan_head(int64_t N, int64_t V) {
+  HeadLayout L{};
+  L.rows = (int)std::min<int64_t>(N, HEAD_ROWS);
+  L.nt = (L.rows + 31) / 32 * 32;  // (the pair's products take multiples of 32 columns)
+  L.n_grp = (int)((V + 31) / 32);
+  L.ld = L.n_grp * 32;
+  L.off_logits = STATUS_BYTES;
+  L.off_mass = L.off_logits + align_up((size_t)L.rows * L.ld * 4, 256);
+  L.off_max = L.off_mass + align_up((size_t)L.n_grp * L.nt * 8, 256);
+  L.bytes = L.off_max + align_up((size_t)L.n_grp * L.nt * 4, 256);
+  return L;
+}
+
+// Runs the chunks; a: settings and outputs.
+cce_status_t run_head(const void* E, const void* C, int64_t N, int64_t D, int64_t V, HeadArgs a, char* ws,
+                      const HeadLayout& L, int sms, cudaStream_t stream) {
+  CUtensorMap tmC, tmE;
+  if (!make_map(&tmC, C, V, D, BM)) return CCE_ERR_CUDA;
+  if (cudaMemsetAsync(ws, 0, STATUS_BYTES, stream) != cudaSuccess) return CCE_ERR_CUDA;
+  a.D = (int)D;
+  a.V = (int)V;
+  a.n_vtile = (int)((V + BN - 1) / BN);
+  a.n_grp = L.n_grp;
+  a.ld = L.ld;
+  a.logits = reinterpret_cast<float*>(ws + L.off_logits);
+  a.gmass = reinterpret_cast<double*>(ws + L.off_mass);
+  a.gmax = reinterpret_cast<float*>(ws + L.off_max);
+  a.status = reinterpret_cast<unsigned long long*>(ws);
+  a.wait_limit_ns = g_wait_limit_ns.load();
+  a.withhold_loads = g_withhold_loads.load();
+  const int grid = 2 * std::min(sms / 2, a.n_vtile);
+  int box = 0;
+  for (int64_t n0 = 0; n0 < N; n0 += HEAD_ROWS) {
+    a.n0 = (int)n0;
+    a.n_rows = (int)std::min<int64_t>(N - n0, HEAD_ROWS);
+    a.nt = (a.n_rows + 31) / 32 * 32;
+    a.stages = head_logits_stages(a.nt);
+    if (a.nt != box && !make_map(&tmE, E, N, D, a.nt / 2)) return CCE_ERR_CUDA;
+    box = a.nt;
+    if (launch_head_logits(tmC, tmE, a, grid, stream) != cudaSuccess ||
+        launch_head_select(a, stream) != cudaSuccess)
+      return CCE_ERR_CUDA;
+  }
+  return CCE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t cce_head_workspace_size(int64_t N, int64_t D, int64_t V) {
+  return head_sizes_ok(N, D, V) ? plan_head(N, V).bytes : 0;
+}
+
+cce_status_t cce_top_logits(const void* E, const void* C, int64_t N, int64_t D, int64_t V, int64_t k, float* values,
+                            int64_t* ids, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!E || !C || !values || !ids || !lse || !workspace) return CCE_ERR_INVALID_ARG;
+  if (!head_sizes_ok(N, D, V) || k <= 0 || k > kMaxTop || k > V) return CCE_ERR_INVALID_ARG;
+  if (!aligned(E, 16) || !aligned(C, 16) || !aligned(values, 4) || !aligned(ids, 8) || !aligned(lse, 4) ||
+      !aligned(workspace, 256))
+    return CCE_ERR_MISALIGNED;
+  const HeadLayout L = plan_head(N, V);
+  const DeviceInfo di = device_info();
+  if (!di.ok || di.sms < 2) return CCE_ERR_UNSUPPORTED_DEVICE;
+  if (workspace_bytes < L.bytes) return CCE_ERR_WORKSPACE_TOO_SMALL;
+  HeadArgs a{};
+  a.temperature_all = 1.f;
+  a.k = (int)k;
+  a.values = values;
+  a.ids = ids;
+  a.lse = lse;
+  return run_head(E, C, N, D, V, a, reinterpret_cast<char*>(workspace), L, di.sms,
+                  reinterpret_cast<cudaStream_t>(stream));
+}
+
+cce_status_t cce_sample(const void* E, const void* C, int64_t N, int64_t D, int64_t V, const float* u,
+                        const cce_sample_settings_t* settings, int64_t* token, float* logp, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  if (!E || !C || !u || !settings || !token || !logp || !workspace) return CCE_ERR_INVALID_ARG;
+  if (!head_sizes_ok(N, D, V)) return CCE_ERR_INVALID_ARG;
+  const cce_sample_settings_t& q = *settings;
+  // one setting for all rows is checked here; per-row settings are read on the device
+  if ((!q.temperature && !(q.temperature_all >= 0.f)) || (!q.top_k && q.top_k_all < 0) ||
+      (!q.top_p && !(q.top_p_all >= 0.f)) || (!q.min_p && !(q.min_p_all >= 0.f && q.min_p_all <= 1.f)))
+    return CCE_ERR_INVALID_ARG;
+  if (!aligned(E, 16) || !aligned(C, 16) || !aligned(u, 4) || !aligned(q.temperature, 4) || !aligned(q.top_k, 4) ||
+      !aligned(q.top_p, 4) || !aligned(q.min_p, 4) || !aligned(token, 8) || !aligned(logp, 4) ||
+      !aligned(workspace, 256))
+    return CCE_ERR_MISALIGNED;
+  const HeadLayout L = plan_head(N, V);
+  const DeviceInfo di = device_info();
+  if (!di.ok || di.sms < 2) return CCE_ERR_UNSUPPORTED_DEVICE;
+  if (workspace_bytes < L.bytes) return CCE_ERR_WORKSPACE_TOO_SMALL;
+  HeadArgs a{};
+  a.u = u;
+  a.temperature = q.temperature;
+  a.top_k = q.top_k;
+  a.top_p = q.top_p;
+  a.min_p = q.min_p;
+  a.temperature_all = q.temperature_all;
+  a.top_k_all = q.top_k_all;
+  a.top_p_all = q.top_p_all;
+  a.min_p_all = q.min_p_all;
+  a.token = token;
+  a.logp = logp;
+  return run_head(E, C, N, D, V, a, reinterpret_cast<char*>(workspace), L, di.sms,
+                  reinterpret_cast<cudaStream_t>(stream));
+}
+
 cce_status_t cce_read_status(const void* workspace, void* stream, cce_counters_t* out) {
   if (!workspace || !out) return CCE_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -1221,6 +1355,7 @@ cce_status_t cce_read_status(const void* workspace, void* stream, cce_counters_t
   out->flat_units = h[ST_FLAT];
   if (h[ST_FLAGS] & SF_TIMEOUT) return CCE_ERR_TIMEOUT;
   if (h[ST_FLAGS] & SF_BAD_LABEL) return CCE_ERR_BAD_LABEL;
+  if (h[ST_FLAGS] & SF_NONFINITE) return CCE_ERR_NONFINITE;
   return CCE_OK;
 }
 
@@ -1234,6 +1369,7 @@ const char* cce_status_string(cce_status_t s) {
     case CCE_ERR_CUDA: return "CCE_ERR_CUDA";
     case CCE_ERR_TIMEOUT: return "CCE_ERR_TIMEOUT";
     case CCE_ERR_BAD_LABEL: return "CCE_ERR_BAD_LABEL";
+    case CCE_ERR_NONFINITE: return "CCE_ERR_NONFINITE";
   }
   return "CCE_ERR_UNKNOWN";
 }

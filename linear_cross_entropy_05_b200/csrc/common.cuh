@@ -52,6 +52,7 @@ constexpr int HDR_BYTES = 256;
 enum StatusFlag : unsigned long long {
   SF_TIMEOUT = 1ull,    // a bounded wait gave up; outputs are incomplete
   SF_BAD_LABEL = 2ull,  // a label outside [0, V) that is not ignore_index
+  SF_NONFINITE = 4ull,  // head_select: a row whose largest logit is infinite or NaN
 };
 constexpr int STATUS_BYTES = 256;
 
@@ -122,6 +123,37 @@ struct DistillFinArgs {
   const unsigned long long* status;
   float* loss;
   float* lse;
+};
+
+// The head's logits of a chunk of tokens and the choice among them (head.cu).
+constexpr int HEAD_ROWS = 256;  // tokens per chunk
+struct HeadArgs {
+  int D, V;
+  int n0, n_rows;      // the chunk's tokens: n0 .. n0 + n_rows - 1, n_rows <= HEAD_ROWS
+  int nt;              // n_rows rounded up to 32: the tiles' token side
+  int n_vtile, n_grp;  // 256-wide vocabulary tiles; groups of 32 entries
+  int stages;
+  int ld;              // floats from one token's logits to the next's
+  float* logits;       // [n_rows][ld]
+  float* gmax;         // [n_grp][nt] largest logit of each group
+  double* gmass;       // [n_grp][nt] sum exp((z - gmax) / T)
+  unsigned long long* status;
+  unsigned long long wait_limit_ns;
+  int withhold_loads;
+  // settings of each row, or one for all where the pointer is null; u is null for top_logits
+  const float* u;
+  const float* temperature;
+  const int* top_k;
+  const float* top_p;
+  const float* min_p;
+  float temperature_all, top_p_all, min_p_all;
+  int top_k_all;
+  int64_t* token;      // [N]
+  float* logp;         // [N]
+  int k;               // top_logits: entries per row
+  float* values;       // [N][k]
+  int64_t* ids;        // [N][k]
+  float* lse;          // [N]
 };
 
 struct PrepArgs {

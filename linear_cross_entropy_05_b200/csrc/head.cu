@@ -1,0 +1,857 @@
+// The head's logits of up to 256 tokens at a time, for choosing among them:
+// the k largest (top_logits) or one drawn token per row (sample).
+//
+//   z_iv = E_i . C_v;  x_iv = z_iv / T_i;
+//   log-probability of v: x_iv - log sum_w exp(x_iw)
+//
+// head_logits   C is read once per 256 tokens, which is what bounds the call
+//               below about 256 tokens (2 V D bytes); above, the products.
+//               The vocabulary is the M side of the tensor-core tiles and the
+//               tokens are the N side, so a batch of 16 multiplies 16 columns
+//               and not 256.  CTA pairs (cta_group::2): 256 vocabulary rows x
+//               up to 256 tokens in TMEM, double buffered; 128 rows of C and
+//               half of the tokens' rows of E per CTA and stage.  The logits
+//               go to the workspace in fp32, and for each group of 32
+//               vocabulary entries the largest one and sum exp(x - largest).
+// head_select   one block per token.  Almost no row needs its logits again:
+//               the groups' largest values bound the k-th largest logit (the
+//               k-th largest group maximum is no larger), so only the groups
+//               that reach the bound are read, and their few candidates are
+//               sorted in shared memory; a draw without filters walks the
+//               groups' sums and reads one group.  Rows that this does not
+//               settle (more than kCap candidates: a wide nucleus, a row full
+//               of ties) take exact passes over the whole row.
+//
+// A drawn token is decided by comparing u with a quotient of sums of up to V
+// exponentials; these sums are formed in double (the groups' in 2^-52 fixed
+// point, so that no order of summation shows), because float sums would move
+// the borders between tokens by more than a rare token's own width.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "ptx.cuh"
+
+namespace cce {
+
+namespace {
+
+constexpr int HL_EPI_WARPS = 8;                  // two per TMEM lane group, alternate 32-token chunks
+constexpr int HL_THREADS = 64 + 32 * HL_EPI_WARPS;
+constexpr int HL_MAX_STAGES = 12;
+constexpr double kLog2e = 1.4426950408889634074;
+
+// Order-preserving map of floats that are not NaN to unsigned.
+__device__ __forceinline__ unsigned order_key(float x) {
+  const unsigned b = __float_as_uint(x);
+  return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float key_value(unsigned k) {
+  return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
+}
+constexpr unsigned kKeyPosInf = 0xff800000u;  // order_key(+inf)
+constexpr unsigned kKeyNegInf = 0x007fffffu;  // order_key(-inf)
+
+__device__ __forceinline__ double row_scale(const HeadArgs& a, int n) {
+  const float t = a.temperature ? a.temperature[n] : a.temperature_all;
+  // (an infinite temperature keeps a scale above 0, so that a logit of -inf still weighs nothing)
+  return t > 0.f ? fmax(kLog2e / (double)t, 1e-300) : kLog2e;  // greedy rows: log-probability at temperature 1
+}
+
+}  // namespace
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(HL_THREADS, 1)
+    head_logits_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmE,
+                       const HeadArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int S = a.stages;
+  const uint32_t stage_bytes = (uint32_t)(A_STAGE_BYTES + a.nt * 64);  // [128 voc][64 d] and [nt / 2 tok][64 d]
+  double* scale = reinterpret_cast<double*>(smem + (size_t)S * stage_bytes);  // [256] log2(e) / T
+  uint64_t* bars = reinterpret_cast<uint64_t*>(scale + 256);
+  uint64_t* full = bars;                    // leader: both CTAs' copies landed
+  uint64_t* empty = full + HL_MAX_STAGES;   // each CTA: stage free again
+  uint64_t* tfull = empty + HL_MAX_STAGES;  // each CTA [2]: accumulator ready
+  uint64_t* tempty = tfull + 2;             // leader [2]: both epilogues done with it
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x >> 1;
+  const int n_pairs = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], 2 * HL_EPI_WARPS);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+  }
+  if (threadIdx.x == 32) {
+    tma_prefetch_map(&tmC);
+    tma_prefetch_map(&tmE);
+  }
+  for (int n = threadIdx.x; n < a.n_rows; n += HL_THREADS) scale[n] = row_scale(a, a.n0 + n);
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const WaitCtl wc{abort_flag, a.wait_limit_ns};
+  const int nkb = (a.D + BK - 1) / BK;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------- TMA producer (both CTAs) ----------------
+      int stage = 0;
+      uint32_t phase = 0, armed = 0;
+      for (int vt = a.withhold_loads ? a.n_vtile : pair; vt < a.n_vtile; vt += n_pairs) {
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, wc)) goto producer_done;
+          uint8_t* X = smem + (size_t)stage * stage_bytes;
+          if (leader) mbar_arrive_expect_tx(&full[stage], 2u * stage_bytes);
+          tma_load_2d_pair(X, &tmC, &full[stage], kb * BK, vt * BN + (int)rank * BM);
+          tma_load_2d_pair(X + A_STAGE_BYTES, &tmE, &full[stage], kb * BK, a.n0 + (int)rank * (a.nt / 2));
+          armed |= 1u << stage;
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    producer_done:
+      if (leader) {
+        int dummy = 0;
+        WaitCtl exit_wc{&dummy, a.wait_limit_ns};
+        for (int s = 0; s < S; ++s)
+          if (armed & (1u << s)) mbar_wait(&full[s], (s < stage) ? phase : (phase ^ 1u), exit_wc);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && leader) {
+      // ---------------- UMMA issuer (leader only) ----------------
+      const uint32_t idesc = idesc_bf16_f32(2 * BM, a.nt, false, false);
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      for (int vt = pair; vt < a.n_vtile; vt += n_pairs) {
+        if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, wc)) goto mma_done;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + (uint32_t)(acc * 256);
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (!mbar_wait(&full[stage], phase, wc)) goto mma_done;
+          tc_fence_after();
+          const uint32_t xa = smem_u32(smem + (size_t)stage * stage_bytes);
+          const uint32_t ya = xa + A_STAGE_BYTES;
+#pragma unroll
+          for (int k = 0; k < BK / 16; ++k)
+            umma_bf16_pair(d_tmem, sdesc_sw128(xa + k * 32, 16, 1024), sdesc_sw128(ya + k * 32, 16, 1024), idesc,
+                           (kb | k) != 0);
+          umma_commit_pair_mc(&empty[stage], 0x3);
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        umma_commit_pair_mc(&tfull[acc], 0x3);
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
+      }
+    mma_done:
+      umma_commit_pair_mc(drain, 0x1);
+      {
+        int dummy = 0;
+        WaitCtl exit_wc{&dummy, a.wait_limit_ns};
+        mbar_wait(drain, 0, exit_wc);
+      }
+    }
+  } else {
+    // ---------------- epilogue: one vocabulary entry (TMEM lane) per thread ----------------
+    const int lg = warp & 3;
+    const int hsel = (warp - 2) >> 2;
+    const uint32_t lane_addr = (uint32_t)(lg * 32) << 16;
+    const uint32_t tempty_leader0 = mapa_shared(smem_u32(&tempty[0]), 0);
+    const uint32_t tempty_leader1 = mapa_shared(smem_u32(&tempty[1]), 0);
+    const int n_chunk = (a.n_rows + 31) / 32;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int vt = pair; vt < a.n_vtile; vt += n_pairs) {
+      const bool ready = __all_sync(0xffffffffu, mbar_wait(&tfull[acc], acc_phase, wc));
+      if (!ready) break;
+      tc_fence_after();
+      const int v = vt * BN + (int)rank * BM + lg * 32 + lane;
+      const int grp = v >> 5;
+      const bool in = v < a.V;
+      for (int c = hsel; c < n_chunk; c += 2) {
+        float x[32];
+        tmem_ld32(tmem_base + lane_addr + (uint32_t)(acc * 256 + c * 32), x);
+        const int n_here = min(32, a.n_rows - c * 32);
+        float* dst = a.logits + (size_t)(c * 32) * a.ld + v;
+        float my_max = 0.f;
+        double my_mass = 0.0;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          if (j < n_here) {  // (uniform)
+            // -0 becomes +0, so that equal logits have equal keys; NaN becomes
+            // +inf, which marks the row (a NaN's sign, and so its key, is not
+            // defined after an addition)
+            float z = x[j] + 0.f;
+            z = z == z ? z : INFINITY;
+            if (in) dst[(size_t)j * a.ld] = z;
+            const unsigned top = __reduce_max_sync(0xffffffffu, in ? order_key(z) : 0u);
+            const float m = key_value(top);
+            const double e = in && z > -INFINITY ? exp2(((double)z - (double)m) * scale[c * 32 + j]) : 0.0;
+            // e in units of 2^-52, its 32 values summed exactly in two words
+            const unsigned long long q = __double2ull_rn(e * 4503599627370496.0);
+            const unsigned hi = __reduce_add_sync(0xffffffffu, (unsigned)(q >> 26));
+            const unsigned lo = __reduce_add_sync(0xffffffffu, (unsigned)q & 0x3ffffffu);
+            if (lane == j) {
+              my_max = m;
+              my_mass = (double)(((unsigned long long)hi << 26) + lo) * (1.0 / 4503599627370496.0);
+            }
+          }
+        }
+        if (lane < n_here && grp < a.n_grp) {
+          a.gmax[(size_t)grp * a.nt + c * 32 + lane] = my_max;
+          a.gmass[(size_t)grp * a.nt + c * 32 + lane] = my_mass;
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(acc ? tempty_leader1 : tempty_leader0);
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
+    }
+  }
+
+  // ---------------- teardown ----------------
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 0) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 512);
+  }
+  if (threadIdx.x == 0 && *abort_flag) atomicOr(a.status + ST_FLAGS, SF_TIMEOUT);
+}
+
+// ----------------------------------------------------------------------------
+// head_select
+// ----------------------------------------------------------------------------
+namespace {
+
+constexpr int HS_THREADS = 512;
+constexpr int HS_WARPS = HS_THREADS / 32;
+constexpr int kCap = 4096;       // candidates sorted in shared memory
+constexpr int kGrpCap = 8192;    // group keys kept in shared memory (V up to 262144; the others are read again)
+
+struct SelectShared {
+  unsigned long long cand[kCap];  // (~key) << 32 | id: ascending = falling logit, then rising id
+  double mass[kCap];
+  double red[HS_WARPS + 1];
+  unsigned hist[256];
+  unsigned ured[HS_WARPS + 1];
+  int count;
+  unsigned found_key;
+  int found_rank;
+  int out_i;
+  double out_d;
+  unsigned gkey[kGrpCap];
+};
+
+// A row's view of head_logits' results.
+struct Row {
+  const float* z;       // [V]
+  const float* gmax;    // [n_grp], stride nt
+  const double* gmass;  // [n_grp], stride nt
+  int V, n_grp, nt;
+  float zmax;
+  double scale;         // log2(e) / T
+};
+
+__device__ __forceinline__ unsigned grp_key(const Row& r, const SelectShared& s, int g) {
+  return g < kGrpCap ? s.gkey[g] : order_key(__ldg(r.gmax + (size_t)g * r.nt));
+}
+// exp((z - zmax) / T)
+__device__ __forceinline__ double mass_of(const Row& r, float z) {
+  return exp2(((double)z - (double)r.zmax) * r.scale);
+}
+
+__device__ __forceinline__ double block_sum(double v, SelectShared& s) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) s.red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  double t = 0.0;
+#pragma unroll
+  for (int i = 0; i < HS_WARPS; ++i) t += s.red[i];
+  return t;
+}
+template <bool MAX>
+__device__ __forceinline__ unsigned block_pick(unsigned v, SelectShared& s) {
+  v = MAX ? __reduce_max_sync(0xffffffffu, v) : __reduce_min_sync(0xffffffffu, v);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) s.ured[threadIdx.x >> 5] = v;
+  __syncthreads();
+  unsigned t = s.ured[0];
+#pragma unroll
+  for (int i = 1; i < HS_WARPS; ++i) t = MAX ? max(t, s.ured[i]) : min(t, s.ured[i]);
+  return t;
+}
+// Exclusive prefix sum of one double per thread; total to every thread.
+__device__ __forceinline__ double block_scan(double v, SelectShared& s, double& total) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  double inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double u = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += u;
+  }
+  __syncthreads();
+  if (lane == 31) s.red[w] = inc;
+  __syncthreads();
+  double before = 0.0;
+  total = 0.0;
+#pragma unroll
+  for (int i = 0; i < HS_WARPS; ++i) {
+    if (i < w) before += s.red[i];
+    total += s.red[i];
+  }
+  const double ex = __shfl_up_sync(0xffffffffu, inc, 1);
+  return before + (lane ? ex : 0.0);
+}
+
+// The want-th largest key (want >= 1) of n keys given by key(i), by four
+// 8-bit digits; `rank` of them with that key belong to the want largest.
+template <typename KeyFn>
+__device__ unsigned radix_select(int n, int want, KeyFn key, SelectShared& s, int& rank) {
+  unsigned prefix = 0u, mask = 0u;
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < 256; i += HS_THREADS) s.hist[i] = 0u;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += HS_THREADS) {
+      const unsigned k = key(i);
+      if ((k & mask) == prefix) atomicAdd(&s.hist[(k >> shift) & 255u], 1u);
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      // lane l holds digits 255 - 8 l .. 248 - 8 l, largest first
+      unsigned part = 0u;
+      for (int j = 0; j < 8; ++j) part += s.hist[255 - 8 * threadIdx.x - j];
+      unsigned inc = part;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned u = __shfl_up_sync(0xffffffffu, inc, o);
+        if ((int)threadIdx.x >= o) inc += u;
+      }
+      unsigned before = inc - part;
+      if (before < (unsigned)want && (unsigned)want <= inc) {
+        for (int j = 0; j < 8; ++j) {
+          const unsigned h = s.hist[255 - 8 * threadIdx.x - j];
+          if ((unsigned)want <= before + h) {
+            s.found_key = 255u - 8u * threadIdx.x - (unsigned)j;
+            s.found_rank = want - (int)before;
+            break;
+          }
+          before += h;
+        }
+      }
+    }
+    __syncthreads();
+    prefix |= s.found_key << shift;
+    mask |= 255u << shift;
+    want = s.found_rank;
+  }
+  rank = want;
+  return prefix;
+}
+
+// Appends every entry with key >= thr to s.cand (as far as it fits); their
+// number (which may exceed kCap) is returned to all threads.
+__device__ int gather_candidates(const Row& r, unsigned thr, SelectShared& s) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  __syncthreads();
+  if (threadIdx.x == 0) s.count = 0;
+  __syncthreads();
+  for (int g0 = w * 32; g0 < r.n_grp; g0 += HS_THREADS) {
+    const int g = g0 + lane;
+    unsigned todo = __ballot_sync(0xffffffffu, g < r.n_grp && grp_key(r, s, g) >= thr);
+    while (todo) {
+      const int b = __ffs(todo) - 1;
+      todo &= todo - 1u;
+      const int v = (g0 + b) * 32 + lane;
+      const unsigned k = v < r.V ? order_key(__ldg(r.z + v)) : 0u;
+      const bool hit = v < r.V && k >= thr;
+      const unsigned hits = __ballot_sync(0xffffffffu, hit);
+      int base = 0;
+      if (lane == 0) base = atomicAdd(&s.count, __popc(hits));
+      base = __shfl_sync(0xffffffffu, base, 0);
+      const int at = base + __popc(hits & ((1u << lane) - 1u));
+      if (hit && at < kCap) s.cand[at] = ((unsigned long long)(~k) << 32) | (unsigned)v;
+    }
+  }
+  __syncthreads();
+  return s.count;
+}
+
+// Sorts s.cand[0 .. n) ascending (n <= kCap; the rest up to a power of two is filled).
+__device__ void sort_candidates(SelectShared& s, int n) {
+  int size2 = 1;
+  while (size2 < n) size2 <<= 1;
+  __syncthreads();
+  for (int i = n + (int)threadIdx.x; i < size2; i += HS_THREADS) s.cand[i] = ~0ull;
+  for (int size = 2; size <= size2; size <<= 1) {
+    for (int stride = size >> 1; stride > 0; stride >>= 1) {
+      __syncthreads();
+      for (int i = threadIdx.x; i < (size2 >> 1); i += HS_THREADS) {
+        const int lo = 2 * i - (i & (stride - 1));
+        const int hi = lo + stride;
+        const bool up = (lo & size) == 0;
+        const unsigned long long ka = s.cand[lo], kb = s.cand[hi];
+        if ((ka > kb) == up) {
+          s.cand[lo] = kb;
+          s.cand[hi] = ka;
+        }
+      }
+    }
+  }
+  __syncthreads();
+}
+__device__ __forceinline__ unsigned cand_key(unsigned long long c) { return ~(unsigned)(c >> 32); }
+
+// Appends, in the order of ids, the entries with key > kappa and the first
+// `ties` entries with key == kappa to s.cand (their number is at most kCap).
+__device__ int gather_exact(const Row& r, unsigned kappa, int ties, SelectShared& s) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  // ties before each warp's contiguous share of the groups
+  const int per = (r.n_grp + HS_WARPS - 1) / HS_WARPS;
+  const int ga = min(r.n_grp, w * per), gb = min(r.n_grp, ga + per);
+  int mine = 0;
+  for (int g = ga; g < gb; ++g) {
+    const int v = g * 32 + lane;
+    mine += __popc(__ballot_sync(0xffffffffu, v < r.V && order_key(__ldg(r.z + v)) == kappa));
+  }
+  __syncthreads();
+  if (lane == 0) s.ured[w] = (unsigned)mine;
+  if (threadIdx.x == 0) s.count = 0;
+  __syncthreads();
+  int seen = 0;
+  for (int i = 0; i < w; ++i) seen += (int)s.ured[i];
+  for (int g = ga; g < gb; ++g) {
+    const int v = g * 32 + lane;
+    const unsigned k = v < r.V ? order_key(__ldg(r.z + v)) : 0u;
+    const unsigned eq = __ballot_sync(0xffffffffu, v < r.V && k == kappa);
+    const bool hit = v < r.V && (k > kappa || (k == kappa && seen + __popc(eq & ((1u << lane) - 1u)) < ties));
+    const unsigned hits = __ballot_sync(0xffffffffu, hit);
+    if (hits) {
+      int base = 0;
+      if (lane == 0) base = atomicAdd(&s.count, __popc(hits));
+      base = __shfl_sync(0xffffffffu, base, 0);
+      const int at = base + __popc(hits & ((1u << lane) - 1u));
+      if (hit && at < kCap) s.cand[at] = ((unsigned long long)(~k) << 32) | (unsigned)v;
+    }
+    seen += __popc(eq);
+  }
+  __syncthreads();
+  return min(s.count, kCap);
+}
+
+// The k largest entries (k <= kCap, k <= V) as candidates: at least these,
+// sorted; their number.
+__device__ int top_candidates(const Row& r, int k, SelectShared& s) {
+  unsigned thr = 0u;
+  int c = kCap + 1, rank;
+  if (r.n_grp >= k) {
+    thr = radix_select(r.n_grp, k, [&](int g) { return grp_key(r, s, g); }, s, rank);
+    c = gather_candidates(r, thr, s);
+  } else if (r.V <= kCap) {
+    c = gather_candidates(r, 0u, s);
+  }
+  if (c > kCap) {
+    thr = radix_select(r.V, k, [&](int v) { return order_key(__ldg(r.z + v)); }, s, rank);
+    c = gather_exact(r, thr, rank, s);
+  }
+  sort_candidates(s, c);
+  return c;
+}
+
+// Sum of exp((z - zmax) / T) over the row's entries with key >= lo.
+__device__ double mass_from(const Row& r, unsigned lo, SelectShared& s) {
+  double m = 0.0;
+  for (int v = threadIdx.x; v < r.V; v += HS_THREADS) {
+    const float z = __ldg(r.z + v);
+    if (order_key(z) >= lo) m += mass_of(r, z);
+  }
+  return block_sum(m, s);
+}
+
+// Settles row-wide what the sorted candidates could not: the prefix, in
+// falling order, that top-k (k > 0), top-p and min-p leave, as a smallest key
+// and how many of the entries with that key belong to it (lowest ids first);
+// then the draw in the order of ids.
+__device__ int wide_draw(const Row& r, int k, double p, double min_p, double u, double total, SelectShared& s) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  unsigned kappa = 0u;
+  int ties = r.V;
+  auto row_key = [&](int v) { return order_key(__ldg(r.z + v)); };
+  if (k > 0 && k < r.V) {
+    kappa = radix_select(r.V, k, row_key, s, ties);
+    total = mass_from(r, kappa + 1u, s) + ties * mass_of(r, key_value(kappa));
+  }
+  if (p < 1.0) {
+    // the largest key whose entries and those above it hold p of the mass,
+    // one bit at a time from the top (never below kappa)
+    const double need = p * total;
+    unsigned key = 0u;
+    for (int bit = 31; bit >= 0; --bit) {
+      const unsigned t = key | (1u << bit);
+      if (t <= kappa || (t <= order_key(r.zmax) && mass_from(r, t, s) >= need)) key = t;
+    }
+    const double above = mass_from(r, key + 1u, s);
+    const double one = mass_of(r, key_value(key));
+    const double left = ceil((need - above) / one);
+    const int n = left < 1.0 ? 1 : (left > (double)r.V ? r.V : (int)left);
+    ties = key == kappa ? min(ties, n) : n;
+    kappa = max(key, kappa);
+  }
+  // min-p leaves a prefix of it too: an entry's own mass decides
+  auto kept = [&](unsigned key, float z, int tie) {
+    return key > kappa || (key == kappa && tie < ties) ? mass_of(r, z) : 0.0;
+  };
+  const int per = (r.n_grp + HS_WARPS - 1) / HS_WARPS;
+  const int ga = min(r.n_grp, w * per), gb = min(r.n_grp, ga + per);
+  int mine = 0;
+  for (int g = ga; g < gb; ++g) {
+    const int v = g * 32 + lane;
+    mine += __popc(__ballot_sync(0xffffffffu, v < r.V && row_key(v) == kappa));
+  }
+  __syncthreads();
+  if (lane == 0) s.ured[w] = (unsigned)mine;
+  __syncthreads();
+  int seen0 = 0;
+  for (int i = 0; i < w; ++i) seen0 += (int)s.ured[i];
+  // this lane's kept mass of group g
+  auto group_mass = [&](int g, int& seen) {
+    const int v = g * 32 + lane;
+    const float z = v < r.V ? __ldg(r.z + v) : 0.f;
+    const unsigned key = v < r.V ? order_key(z) : 0u;
+    const unsigned eq = __ballot_sync(0xffffffffu, v < r.V && key == kappa);
+    double e = v < r.V ? kept(key, z, seen + __popc(eq & ((1u << lane) - 1u))) : 0.0;
+    if (e < min_p) e = 0.0;
+    seen += __popc(eq);
+    return e;
+  };
+  double m = 0.0;
+  int seen = seen0;
+  for (int g = ga; g < gb; ++g) m += group_mass(g, seen);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+  __syncthreads();
+  if (lane == 0) s.red[w] = m;
+  if (threadIdx.x == 0) s.out_i = -1;
+  __syncthreads();
+  double before = 0.0, all = 0.0;
+  int last_warp = 0;
+  for (int i = 0; i < HS_WARPS; ++i) {
+    if (i < w) before += s.red[i];
+    all += s.red[i];
+    if (s.red[i] > 0.0) last_warp = i;
+  }
+  const double target = u * all;
+  const bool here = m > 0.0 && before <= target && (target < before + m || w == last_warp);
+  const bool fallback = w == last_warp && !(target < all);
+  if (here || fallback) {
+    double run = before;
+    int pick = -1, last = -1;
+    seen = seen0;
+    for (int g = ga; g < gb && pick < 0; ++g) {
+      double e = group_mass(g, seen);
+      const unsigned any = __ballot_sync(0xffffffffu, e > 0.0);
+      if (any) last = g * 32 + 31 - __clz((int)any);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const double x = __shfl_up_sync(0xffffffffu, e, o);
+        if (lane >= o) e += x;
+      }
+      const unsigned over = __ballot_sync(0xffffffffu, run + e > target) & any;
+      if (over) pick = g * 32 + __ffs((int)over) - 1;
+      run += __shfl_sync(0xffffffffu, e, 31);
+    }
+    if (lane == 0) s.out_i = pick >= 0 ? pick : last;
+  }
+  __syncthreads();
+  return s.out_i;
+}
+
+// Draw without filters: the first id whose cumulated mass passes u times the
+// whole, from the groups' sums and one group's logits.
+__device__ int plain_draw(const Row& r, double u, SelectShared& s) {
+  const int lane = threadIdx.x & 31;
+  const int per = (r.n_grp + HS_THREADS - 1) / HS_THREADS;
+  const int ga = min(r.n_grp, (int)threadIdx.x * per), gb = min(r.n_grp, ga + per);
+  auto weight = [&](int g) {
+    return __ldg(r.gmass + (size_t)g * r.nt) * mass_of(r, key_value(grp_key(r, s, g)));
+  };
+  double m = 0.0;
+  for (int g = ga; g < gb; ++g) m += weight(g);
+  double total;
+  const double before = block_scan(m, s, total);
+  const double target = u * total;
+  // the thread whose share holds the target: the last that begins at or below it
+  const unsigned mine = m > 0.0 && before <= target ? threadIdx.x + 1u : 0u;
+  const unsigned owner = block_pick<true>(mine, s);
+  if (threadIdx.x + 1u == owner || (owner == 0u && threadIdx.x == 0)) {
+    double run = before;
+    int g = ga, best = ga;
+    double left = 0.0;
+    for (; g < gb; ++g) {
+      const double x = weight(g);
+      if (x > 0.0) {
+        best = g;
+        left = target - run;
+        if (run + x > target) break;
+      }
+      run += x;
+    }
+    s.out_i = best;
+    s.out_d = left;
+  }
+  __syncthreads();
+  const int g = s.out_i;
+  const double left = s.out_d;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int v = g * 32 + lane;
+    const double own = v < r.V ? mass_of(r, __ldg(r.z + v)) : 0.0;
+    double inc = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    const unsigned any = __ballot_sync(0xffffffffu, own > 0.0);
+    const unsigned over = __ballot_sync(0xffffffffu, own > 0.0 && inc > left);
+    const int l = over ? __ffs((int)over) - 1 : 31 - __clz((int)any);
+    if (lane == 0) s.out_i = g * 32 + l;
+  }
+  __syncthreads();
+  return s.out_i;
+}
+
+// Draw from sorted candidates that hold every kept entry; k = 0: no top-k.
+__device__ int draw_from_candidates(const Row& r, int c, int k, double p, double min_p, double u, double total,
+                                    SelectShared& s) {
+  if (k > 0) c = min(c, k);
+  constexpr int PER = kCap / HS_THREADS;
+  // masses in falling order and what comes before each
+  const int i0 = threadIdx.x * PER;
+  double e[PER], m = 0.0;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    e[j] = i0 + j < c ? mass_of(r, key_value(cand_key(s.cand[i0 + j]))) : 0.0;
+    m += e[j];
+  }
+  double sum;
+  double before = block_scan(m, s, sum);
+  if (k > 0) total = sum;
+  int keep = 0;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    if (i0 + j < c && (i0 + j == 0 || p >= 1.0 || before < p * total) && e[j] >= min_p) ++keep;
+    before += e[j];
+  }
+  // (both filters leave a prefix)
+  const int n = (int)(block_sum((double)keep, s) + 0.5);
+  if (n <= 1) return (int)(unsigned)s.cand[0];
+  // the kept entries in the order of ids; their keys are needed for the masses
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += HS_THREADS) {
+    const unsigned long long cc = s.cand[i];
+    s.mass[i] = mass_of(r, key_value(cand_key(cc)));
+    s.cand[i] = ((cc & 0xffffffffull) << 32) | (unsigned)i;
+  }
+  sort_candidates(s, n);
+  m = 0.0;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    e[j] = i0 + j < n ? s.mass[(unsigned)s.cand[i0 + j]] : 0.0;
+    m += e[j];
+  }
+  before = block_scan(m, s, sum);
+  const double target = u * sum;
+  unsigned pick = 0xffffffffu;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    before += e[j];
+    if (i0 + j < n && e[j] > 0.0 && before > target) pick = min(pick, (unsigned)(i0 + j));
+  }
+  pick = block_pick<false>(pick, s);
+  if (pick == 0xffffffffu) pick = (unsigned)(n - 1);
+  return (int)(s.cand[pick] >> 32);
+}
+
+__device__ int sample_row(const Row& r, int k, double p, double min_p, double u, double total, bool greedy,
+                          unsigned top_key, SelectShared& s) {
+  if (k >= r.V || k < 0) k = 0;
+  if (greedy || k == 1) {
+    // the lowest id among the largest logits
+    unsigned g_first = 0xffffffffu;
+    for (int g = threadIdx.x; g < r.n_grp; g += HS_THREADS)
+      if (grp_key(r, s, g) == top_key) {
+        g_first = (unsigned)g;
+        break;
+      }
+    const int g = (int)block_pick<false>(g_first, s);
+    const int v = g * 32 + (int)(threadIdx.x & 31);
+    const unsigned eq = __ballot_sync(0xffffffffu, v < r.V && order_key(__ldg(r.z + v)) == top_key);
+    return g * 32 + __ffs((int)eq) - 1;
+  }
+  if (k == 0 && p >= 1.0 && !(min_p > 0.0)) return plain_draw(r, u, s);
+  if (k > 0 && k <= kCap) return draw_from_candidates(r, top_candidates(r, k, s), k, p, min_p, u, total, s);
+  if (k == 0) {
+    // entries below min_p of the largest are out (a little slack: their own
+    // masses decide); of the others, groups in growing numbers until their
+    // candidates hold p of the mass
+    unsigned floor_key = 0u;
+    if (min_p > 0.0) {
+      const double t = (double)r.zmax + log2(min_p) / r.scale;
+      floor_key = min(top_key, order_key((float)(t - 1e-6 * (fabs(t) + fabs((double)r.zmax) + 1.0))));
+    }
+    for (int want = 64; want <= 4096; want <<= 3) {
+      unsigned thr = 0u;
+      int rank;
+      if (want < r.n_grp) thr = radix_select(r.n_grp, want, [&](int g) { return grp_key(r, s, g); }, s, rank);
+      if (p >= 1.0) thr = 0u;
+      thr = max(thr, floor_key);
+      const int c = gather_candidates(r, thr, s);
+      if (c > kCap) break;
+      double m = 0.0;
+      for (int i = threadIdx.x; i < c; i += HS_THREADS) m += mass_of(r, key_value(cand_key(s.cand[i])));
+      m = block_sum(m, s);
+      if (thr == floor_key || m >= p * total) {
+        sort_candidates(s, c);
+        return draw_from_candidates(r, c, 0, p, min_p, u, total, s);
+      }
+    }
+  }
+  return wide_draw(r, k, p, min_p, u, total, s);
+}
+
+}  // namespace
+
+__global__ void __launch_bounds__(HS_THREADS) head_select_kernel(const HeadArgs a) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  SelectShared& s = *reinterpret_cast<SelectShared*>(smem_raw);
+  const int n = blockIdx.x;          // row of this chunk
+  const int row = a.n0 + n;
+  const float qnan = __int_as_float(0x7fc00000);
+  Row r;
+  r.z = a.logits + (size_t)n * a.ld;
+  r.gmax = a.gmax + n;
+  r.gmass = a.gmass + n;
+  r.V = a.V;
+  r.n_grp = a.n_grp;
+  r.nt = a.nt;
+  r.scale = row_scale(a, row);
+
+  unsigned top = 0u;
+  for (int g = threadIdx.x; g < r.n_grp; g += HS_THREADS) {
+    const unsigned k = order_key(__ldg(r.gmax + (size_t)g * r.nt));
+    if (g < kGrpCap) s.gkey[g] = k;
+    top = max(top, k);
+  }
+  top = block_pick<true>(top, s);
+  r.zmax = key_value(top);
+  const bool timeout = (a.status[ST_FLAGS] & SF_TIMEOUT) != 0;
+  const bool broken = top >= kKeyPosInf || top <= kKeyNegInf;  // an infinite (or NaN) logit on top
+  if (timeout || broken) {
+    if (threadIdx.x == 0 && !timeout) atomicOr(a.status + ST_FLAGS, SF_NONFINITE);
+    if (a.u) {
+      if (threadIdx.x == 0) {
+        a.token[row] = -1;
+        a.logp[row] = qnan;
+      }
+    } else {
+      for (int i = threadIdx.x; i < a.k; i += HS_THREADS) {
+        a.values[(size_t)row * a.k + i] = qnan;
+        a.ids[(size_t)row * a.k + i] = -1;
+      }
+      if (threadIdx.x == 0) a.lse[row] = qnan;
+    }
+    return;
+  }
+  double m = 0.0;
+  for (int g = threadIdx.x; g < r.n_grp; g += HS_THREADS)
+    m += __ldg(r.gmass + (size_t)g * r.nt) * mass_of(r, key_value(grp_key(r, s, g)));
+  const double total = block_sum(m, s);
+  constexpr double kLn2 = 0.69314718055994530942;
+
+  if (!a.u) {
+    const int c = top_candidates(r, a.k, s);
+    for (int i = threadIdx.x; i < a.k; i += HS_THREADS) {
+      const unsigned long long cc = i < c ? s.cand[i] : 0ull;
+      a.values[(size_t)row * a.k + i] = key_value(cand_key(cc));
+      a.ids[(size_t)row * a.k + i] = (int64_t)(unsigned)cc;
+    }
+    if (threadIdx.x == 0) a.lse[row] = (float)((double)r.zmax + log(total));
+    return;
+  }
+  const float t = a.temperature ? a.temperature[row] : a.temperature_all;
+  const int k = a.top_k ? a.top_k[row] : a.top_k_all;
+  // settings outside their ranges act as the nearest inside; NaN as "off" (u: 0)
+  double p = (double)(a.top_p ? a.top_p[row] : a.top_p_all);
+  p = p < 1.0 ? fmax(p, 0.0) : 1.0;
+  double min_p = (double)(a.min_p ? a.min_p[row] : a.min_p_all);
+  min_p = min_p > 0.0 ? fmin(min_p, 1.0) : 0.0;
+  const double u = fmax((double)a.u[row], 0.0);
+  const int token = sample_row(r, k, p, min_p, u, total, !(t > 0.f), top, s);
+  if (threadIdx.x == 0) {
+    a.token[row] = token;
+    a.logp[row] = (float)(((double)__ldg(r.z + token) - (double)r.zmax) * r.scale * kLn2 - log(total));
+  }
+}
+
+int head_logits_stages(int nt) {
+  const int fit = (227 * 1024 - 1024 - 2048 - 512) / (A_STAGE_BYTES + nt * 64);
+  return fit < HL_MAX_STAGES ? fit : HL_MAX_STAGES;
+}
+
+// tmC: C in boxes of {64, 128}; tmE: E in boxes of {64, nt / 2}; grid: an even number of CTAs.
+cudaError_t launch_head_logits(const CUtensorMap& tmC, const CUtensorMap& tmE, const HeadArgs& a, int grid,
+                               cudaStream_t stream) {
+  const size_t smem = 1024 + (size_t)a.stages * (A_STAGE_BYTES + a.nt * 64) + 2048 + 512;
+  cudaError_t e = cudaFuncSetAttribute(head_logits_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  head_logits_kernel<<<grid, HL_THREADS, smem, stream>>>(tmC, tmE, a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_head_select(const HeadArgs& a, cudaStream_t stream) {
+  const size_t smem = sizeof(SelectShared);
+  cudaError_t e = cudaFuncSetAttribute(head_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  head_select_kernel<<<a.n_rows, HS_THREADS, smem, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace cce

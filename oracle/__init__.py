@@ -359,3 +359,39 @@ def distill(E, C, ids, teacher, temperature=1.0, ignore_index=-100, dloss=None):
     np.add.at(target, (np.broadcast_to(rows, at.shape), at), p)
     G = (np.exp(x - lse[:, None]) - target) * (T * np.asarray(dloss, dtype=np.float64) * has)[:, None]
     return loss, lse, G @ C, G.T @ E, G
+
+
+# ---------------------------------------------------------------------------
+# choosing among a row of logits
+# ---------------------------------------------------------------------------
+
+def falling_order(z):
+    """Indices of z in falling order, equal values by rising index."""
+    return np.lexsort((np.arange(z.size), -z))
+
+
+def sample_row(z, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
+    """(token, log-probability) of one row of fp64 logits: top-k, top-p and
+    min-p in falling order, then the first id, in the order of ids, whose
+    cumulated kept mass is above u times the whole."""
+    x = z / temperature if temperature > 0 else z
+    logp = x - x.max() - math.log(np.exp(x - x.max()).sum())
+    if not temperature > 0:
+        token = int(np.argmax(z))
+        return token, logp[token]
+    order = falling_order(z)
+    if 0 < top_k < z.size:
+        order = order[:top_k]
+    mass = np.exp(x[order] - x[order[0]])
+    if top_p < 1:
+        before = np.cumsum(mass) - mass
+        keep = before < top_p * mass.sum()
+        keep[0] = True
+        order, mass = order[keep], mass[keep]
+    order = order[mass >= min(min_p, 1.0)]
+    ids = np.sort(order)
+    total = np.cumsum(np.exp(x[ids] - x.max()))
+    at = int((total <= u * total[-1]).sum())
+    live = np.flatnonzero(np.diff(total, prepend=0.0) > 0)
+    token = int(ids[min(at, int(live[-1]))])
+    return token, logp[token]
