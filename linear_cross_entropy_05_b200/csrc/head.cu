@@ -53,6 +53,47 @@ __device__ __forceinline__ float key_value(unsigned k) {
 constexpr unsigned kKeyPosInf = 0xff800000u;  // order_key(+inf)
 constexpr unsigned kKeyNegInf = 0x007fffffu;  // order_key(-inf)
 
+// 2^-t for t >= 0 (0 above 1000), off by a few units of 2^-53: t = k / 64 + r
+// with |r| <= 1 / 128, 2^-(k mod 64) / 64 from a table and 2^-r from its series
+// up to r^5 (the next term is below 4e-17).  About a third of the double
+// operations of a general exp2.
+constexpr int kExpTab = 64;
+__device__ __forceinline__ void fill_exp_table(double* tab) {
+  if (threadIdx.x < kExpTab) tab[threadIdx.x] = exp2(-(double)threadIdx.x / kExpTab);
+}
+__device__ __forceinline__ double exp2_neg(double t, const double* tab) {
+  constexpr double kRound = 6755399441055744.0 / kExpTab;  // 1.5 2^52 / 64: adding it rounds to multiples of 1 / 64
+  const double u = t + kRound;
+  const int k = __double2loint(u);
+  const double r = t - (u - kRound);
+  // (-ln 2)^n / n!
+  double q = fma(r, -1.3333558146428443e-3, 9.6181291076284772e-3);
+  q = fma(q, r, -5.5504108664821580e-2);
+  q = fma(q, r, 2.4022650695910071e-1);
+  q = fma(q, r, -6.9314718055994531e-1);
+  q = fma(q, r, 1.0);
+  q *= tab[k & (kExpTab - 1)];
+  const double e = __hiloint2double(__double2hiint(q) - ((k >> 6) << 20), __double2loint(q));
+  return t < 1000.0 ? e : 0.0;
+}
+
+// Whether a row's token hangs on sums over the whole vocabulary: a draw
+// without top-k whose mass is shared out (no filter, or top-p).  Its groups'
+// sums are formed in double; for the other rows they only enter the
+// log-sum-exp, and float exponentials do.
+__device__ __forceinline__ bool row_exact(const HeadArgs& a, int row) {
+  if (!a.u || !((a.temperature ? a.temperature[row] : a.temperature_all) > 0.f)) return false;
+  const int k = a.top_k ? a.top_k[row] : a.top_k_all;
+  if (k > 0 && k < a.V) return false;
+  return (a.top_p ? a.top_p[row] : a.top_p_all) < 1.f || !((a.min_p ? a.min_p[row] : a.min_p_all) > 0.f);
+}
+
+__device__ __forceinline__ float warp_max(float x) {
+  float m;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
+  return m;
+}
+
 __device__ __forceinline__ double row_scale(const HeadArgs& a, int n) {
   const float t = a.temperature ? a.temperature[n] : a.temperature_all;
   // (an infinite temperature keeps a scale above 0, so that a logit of -inf still weighs nothing)
@@ -69,7 +110,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(HL_THREADS, 1)
   const int S = a.stages;
   const uint32_t stage_bytes = (uint32_t)(A_STAGE_BYTES + a.nt * 64);  // [128 voc][64 d] and [nt / 2 tok][64 d]
   double* scale = reinterpret_cast<double*>(smem + (size_t)S * stage_bytes);  // [256] log2(e) / T
-  uint64_t* bars = reinterpret_cast<uint64_t*>(scale + 256);
+  double* tab = scale + HEAD_ROWS;
+  unsigned* exact = reinterpret_cast<unsigned*>(tab + kExpTab);               // [8] a bit per row: row_exact
+  uint64_t* bars = reinterpret_cast<uint64_t*>(exact + HEAD_ROWS / 32);
   uint64_t* full = bars;                    // leader: both CTAs' copies landed
   uint64_t* empty = full + HL_MAX_STAGES;   // each CTA: stage free again
   uint64_t* tfull = empty + HL_MAX_STAGES;  // each CTA [2]: accumulator ready
@@ -106,7 +149,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(HL_THREADS, 1)
     tma_prefetch_map(&tmC);
     tma_prefetch_map(&tmE);
   }
-  for (int n = threadIdx.x; n < a.n_rows; n += HL_THREADS) scale[n] = row_scale(a, a.n0 + n);
+  if (threadIdx.x < HEAD_ROWS) {  // (whole warps)
+    const int n = threadIdx.x;
+    const bool live = n < a.n_rows;
+    scale[n] = live ? row_scale(a, a.n0 + n) : 1.0;
+    const unsigned bits = __ballot_sync(0xffffffffu, live && row_exact(a, a.n0 + n));
+    if (lane == 0) exact[warp] = bits;
+  }
+  fill_exp_table(tab);
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
@@ -202,27 +252,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(HL_THREADS, 1)
         tmem_ld32(tmem_base + lane_addr + (uint32_t)(acc * 256 + c * 32), x);
         const int n_here = min(32, a.n_rows - c * 32);
         float* dst = a.logits + (size_t)(c * 32) * a.ld + v;
+        const bool in_double = exact[c] != 0u;  // (for the whole chunk)
         float my_max = 0.f;
         double my_mass = 0.0;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          if (j < n_here) {  // (uniform)
-            // -0 becomes +0, so that equal logits have equal keys; NaN becomes
-            // +inf, which marks the row (a NaN's sign, and so its key, is not
-            // defined after an addition)
-            float z = x[j] + 0.f;
-            z = z == z ? z : INFINITY;
-            if (in) dst[(size_t)j * a.ld] = z;
-            const unsigned top = __reduce_max_sync(0xffffffffu, in ? order_key(z) : 0u);
-            const float m = key_value(top);
-            const double e = in && z > -INFINITY ? exp2(((double)z - (double)m) * scale[c * 32 + j]) : 0.0;
-            // e in units of 2^-52, its 32 values summed exactly in two words
-            const unsigned long long q = __double2ull_rn(e * 4503599627370496.0);
-            const unsigned hi = __reduce_add_sync(0xffffffffu, (unsigned)(q >> 26));
-            const unsigned lo = __reduce_add_sync(0xffffffffu, (unsigned)q & 0x3ffffffu);
-            if (lane == j) {
-              my_max = m;
-              my_mass = (double)(((unsigned long long)hi << 26) + lo) * (1.0 / 4503599627370496.0);
+        for (int j0 = 0; j0 < 32; j0 += 8) {
+          if (j0 < n_here) {
+            float m[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              // -0 becomes +0, so that equal logits have equal keys; NaN becomes
+              // +inf, which marks the row (a NaN's sign, and so its key, is not
+              // defined after an addition)
+              float z = x[j0 + j] + 0.f;
+              z = z == z ? z : INFINITY;
+              if (in && j0 + j < n_here) dst[(size_t)(j0 + j) * a.ld] = z;
+              x[j0 + j] = in ? z : -INFINITY;
+              m[j] = warp_max(x[j0 + j]);
+            }
+            // each exponential in fixed point, so that the 32 of a group are
+            // summed exactly by integer reductions: units of 2^-26 from float,
+            // of 2^-51 in two words from double
+            if (!in_double) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const float e = ex2_approx((x[j0 + j] - m[j]) * (float)scale[c * 32 + j0 + j]);
+                const unsigned sum = __reduce_add_sync(0xffffffffu, __float2uint_rn(e * 67108864.f));
+                if (lane == j0 + j) {
+                  my_max = m[j];
+                  my_mass = (double)sum * (1.0 / 67108864.0);
+                }
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const double t = ((double)m[j] - (double)x[j0 + j]) * scale[c * 32 + j0 + j];
+                const double w = exp2_neg(t, tab) + 2.0;  // in [2, 3]: the fraction's 52 bits are e in units of 2^-51
+                const unsigned whi = (unsigned)__double2hiint(w) & 0xfffffu, wlo = (unsigned)__double2loint(w);
+                const unsigned hi = __reduce_add_sync(0xffffffffu, (whi << 6) | (wlo >> 26));
+                const unsigned lo = __reduce_add_sync(0xffffffffu, wlo & 0x3ffffffu);
+                if (lane == j0 + j) {
+                  my_max = m[j];
+                  my_mass = ((double)hi * 67108864.0 + (double)lo) * (1.0 / 2251799813685248.0);
+                }
+              }
             }
           }
         }
@@ -265,10 +338,14 @@ constexpr int kGrpCap = 8192;    // group keys kept in shared memory (V up to 26
 
 struct SelectShared {
   unsigned long long cand[kCap];  // (~key) << 32 | id: ascending = falling logit, then rising id
-  double mass[kCap];
+  union {
+    double mass[kCap];
+    int list[2 * kCap];           // groups to read
+  };
+  double tab[kExpTab];
   double red[HS_WARPS + 1];
   unsigned hist[256];
-  unsigned ured[HS_WARPS + 1];
+  unsigned ured[3][HS_WARPS];
   int count;
   unsigned found_key;
   int found_rank;
@@ -285,6 +362,7 @@ struct Row {
   int V, n_grp, nt;
   float zmax;
   double scale;         // log2(e) / T
+  const double* tab;
 };
 
 __device__ __forceinline__ unsigned grp_key(const Row& r, const SelectShared& s, int g) {
@@ -292,7 +370,7 @@ __device__ __forceinline__ unsigned grp_key(const Row& r, const SelectShared& s,
 }
 // exp((z - zmax) / T)
 __device__ __forceinline__ double mass_of(const Row& r, float z) {
-  return exp2(((double)z - (double)r.zmax) * r.scale);
+  return exp2_neg(((double)r.zmax - (double)z) * r.scale, r.tab);
 }
 
 __device__ __forceinline__ double block_sum(double v, SelectShared& s) {
@@ -310,11 +388,11 @@ template <bool MAX>
 __device__ __forceinline__ unsigned block_pick(unsigned v, SelectShared& s) {
   v = MAX ? __reduce_max_sync(0xffffffffu, v) : __reduce_min_sync(0xffffffffu, v);
   __syncthreads();
-  if ((threadIdx.x & 31) == 0) s.ured[threadIdx.x >> 5] = v;
+  if ((threadIdx.x & 31) == 0) s.ured[0][threadIdx.x >> 5] = v;
   __syncthreads();
-  unsigned t = s.ured[0];
+  unsigned t = s.ured[0][0];
 #pragma unroll
-  for (int i = 1; i < HS_WARPS; ++i) t = MAX ? max(t, s.ured[i]) : min(t, s.ured[i]);
+  for (int i = 1; i < HS_WARPS; ++i) t = MAX ? max(t, s.ured[0][i]) : min(t, s.ured[0][i]);
   return t;
 }
 // Exclusive prefix sum of one double per thread; total to every thread.
@@ -386,28 +464,100 @@ __device__ unsigned radix_select(int n, int want, KeyFn key, SelectShared& s, in
   return prefix;
 }
 
+// A key that at least `want` group maxima reach (1 <= want <= n_grp), and not
+// many more: three counts a pass split the keys between one that is reached
+// often enough and one that is not into four, until the number is within half
+// of `want` or the keys are exhausted.  (A radix select's first digits put
+// every group into one bin: 8000 additions to one word a digit, 76 us a row.)
+__device__ unsigned group_threshold(const Row& r, int want, unsigned top, unsigned bottom, SelectShared& s) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  unsigned lo = bottom, hi = top + 1u;  // count(>= lo) >= want > count(>= hi)
+  const int enough = want + want / 2 + 16;
+  while (hi - lo > 1u) {
+    const unsigned step = max(1u, (hi - lo) / 4u);
+    const unsigned t1 = lo + step, t2 = min(hi, t1 + step), t3 = min(hi, t2 + step);
+    unsigned c1 = 0u, c2 = 0u, c3 = 0u;
+    for (int g = threadIdx.x; g < r.n_grp; g += HS_THREADS) {
+      const unsigned k = grp_key(r, s, g);
+      c1 += k >= t1;
+      c2 += k >= t2;
+      c3 += k >= t3;
+    }
+    c1 = __reduce_add_sync(0xffffffffu, c1);
+    c2 = __reduce_add_sync(0xffffffffu, c2);
+    c3 = __reduce_add_sync(0xffffffffu, c3);
+    __syncthreads();
+    if (lane == 0) {
+      s.ured[0][w] = c1;
+      s.ured[1][w] = c2;
+      s.ured[2][w] = c3;
+    }
+    __syncthreads();
+    c1 = c2 = c3 = 0u;
+#pragma unroll
+    for (int i = 0; i < HS_WARPS; ++i) {
+      c1 += s.ured[0][i];
+      c2 += s.ured[1][i];
+      c3 += s.ured[2][i];
+    }
+    int c_lo = INT_MAX;
+    if ((int)c3 >= want) {
+      lo = t3;
+      c_lo = (int)c3;
+    } else if ((int)c2 >= want) {
+      lo = t2;
+      hi = t3;
+      c_lo = (int)c2;
+    } else if ((int)c1 >= want) {
+      lo = t1;
+      hi = t2;
+      c_lo = (int)c1;
+    } else {
+      hi = t1;
+    }
+    if (c_lo <= enough) break;
+  }
+  return lo;
+}
+
 // Appends every entry with key >= thr to s.cand (as far as it fits); their
-// number (which may exceed kCap) is returned to all threads.
+// number, or one above kCap, is returned to all threads.
 __device__ int gather_candidates(const Row& r, unsigned thr, SelectShared& s) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   __syncthreads();
-  if (threadIdx.x == 0) s.count = 0;
+  if (threadIdx.x == 0) {
+    s.count = 0;
+    s.found_rank = 0;
+  }
   __syncthreads();
-  for (int g0 = w * 32; g0 < r.n_grp; g0 += HS_THREADS) {
-    const int g = g0 + lane;
-    unsigned todo = __ballot_sync(0xffffffffu, g < r.n_grp && grp_key(r, s, g) >= thr);
-    while (todo) {
-      const int b = __ffs(todo) - 1;
-      todo &= todo - 1u;
-      const int v = (g0 + b) * 32 + lane;
-      const unsigned k = v < r.V ? order_key(__ldg(r.z + v)) : 0u;
-      const bool hit = v < r.V && k >= thr;
+  for (int g = threadIdx.x; g < r.n_grp; g += HS_THREADS)
+    if (grp_key(r, s, g) >= thr) {
+      const int at = atomicAdd(&s.found_rank, 1);
+      if (at < 2 * kCap) s.list[at] = g;
+    }
+  __syncthreads();
+  const int n_list = s.found_rank;
+  if (n_list > kCap) return kCap + 1;  // a candidate at least from each
+  for (int i = w; i < n_list; i += 4 * HS_WARPS) {
+    // four groups a turn, so that their loads overlap
+    float z[4];
+    int v[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int at = i + q * HS_WARPS;
+      v[q] = at < n_list ? s.list[at] * 32 + lane : r.V;
+      z[q] = v[q] < r.V ? __ldg(r.z + v[q]) : 0.f;
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const unsigned k = order_key(z[q]);
+      const bool hit = v[q] < r.V && k >= thr;
       const unsigned hits = __ballot_sync(0xffffffffu, hit);
       int base = 0;
-      if (lane == 0) base = atomicAdd(&s.count, __popc(hits));
+      if (lane == 0 && hits) base = atomicAdd(&s.count, __popc(hits));
       base = __shfl_sync(0xffffffffu, base, 0);
       const int at = base + __popc(hits & ((1u << lane) - 1u));
-      if (hit && at < kCap) s.cand[at] = ((unsigned long long)(~k) << 32) | (unsigned)v;
+      if (hit && at < kCap) s.cand[at] = ((unsigned long long)(~k) << 32) | (unsigned)v[q];
     }
   }
   __syncthreads();
@@ -416,6 +566,20 @@ __device__ int gather_candidates(const Row& r, unsigned thr, SelectShared& s) {
 
 // Sorts s.cand[0 .. n) ascending (n <= kCap; the rest up to a power of two is filled).
 __device__ void sort_candidates(SelectShared& s, int n) {
+  __syncthreads();
+  if (n <= HS_THREADS) {
+    // every entry counts the smaller ones (all differ): no steps to wait for
+    const int i = threadIdx.x;
+    const unsigned long long mine = i < n ? s.cand[i] : 0ull;
+    int rank = 0;
+    if ((i & ~31) < n)
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) rank += s.cand[j] < mine;
+    __syncthreads();
+    if (i < n) s.cand[rank] = mine;
+    __syncthreads();
+    return;
+  }
   int size2 = 1;
   while (size2 < n) size2 <<= 1;
   __syncthreads();
@@ -452,11 +616,11 @@ __device__ int gather_exact(const Row& r, unsigned kappa, int ties, SelectShared
     mine += __popc(__ballot_sync(0xffffffffu, v < r.V && order_key(__ldg(r.z + v)) == kappa));
   }
   __syncthreads();
-  if (lane == 0) s.ured[w] = (unsigned)mine;
+  if (lane == 0) s.ured[0][w] = (unsigned)mine;
   if (threadIdx.x == 0) s.count = 0;
   __syncthreads();
   int seen = 0;
-  for (int i = 0; i < w; ++i) seen += (int)s.ured[i];
+  for (int i = 0; i < w; ++i) seen += (int)s.ured[0][i];
   for (int g = ga; g < gb; ++g) {
     const int v = g * 32 + lane;
     const unsigned k = v < r.V ? order_key(__ldg(r.z + v)) : 0u;
@@ -478,17 +642,14 @@ __device__ int gather_exact(const Row& r, unsigned kappa, int ties, SelectShared
 
 // The k largest entries (k <= kCap, k <= V) as candidates: at least these,
 // sorted; their number.
-__device__ int top_candidates(const Row& r, int k, SelectShared& s) {
-  unsigned thr = 0u;
+__device__ int top_candidates(const Row& r, int k, unsigned top, unsigned bottom, SelectShared& s) {
   int c = kCap + 1, rank;
-  if (r.n_grp >= k) {
-    thr = radix_select(r.n_grp, k, [&](int g) { return grp_key(r, s, g); }, s, rank);
-    c = gather_candidates(r, thr, s);
-  } else if (r.V <= kCap) {
+  if (r.n_grp >= k)
+    c = gather_candidates(r, group_threshold(r, k, top, bottom, s), s);
+  else if (r.V <= kCap)
     c = gather_candidates(r, 0u, s);
-  }
   if (c > kCap) {
-    thr = radix_select(r.V, k, [&](int v) { return order_key(__ldg(r.z + v)); }, s, rank);
+    const unsigned thr = radix_select(r.V, k, [&](int v) { return order_key(__ldg(r.z + v)); }, s, rank);
     c = gather_exact(r, thr, rank, s);
   }
   sort_candidates(s, c);
@@ -546,10 +707,10 @@ __device__ int wide_draw(const Row& r, int k, double p, double min_p, double u, 
     mine += __popc(__ballot_sync(0xffffffffu, v < r.V && row_key(v) == kappa));
   }
   __syncthreads();
-  if (lane == 0) s.ured[w] = (unsigned)mine;
+  if (lane == 0) s.ured[0][w] = (unsigned)mine;
   __syncthreads();
   int seen0 = 0;
-  for (int i = 0; i < w; ++i) seen0 += (int)s.ured[i];
+  for (int i = 0; i < w; ++i) seen0 += (int)s.ured[0][i];
   // this lane's kept mass of group g
   auto group_mass = [&](int g, int& seen) {
     const int v = g * 32 + lane;
@@ -604,44 +765,61 @@ __device__ int wide_draw(const Row& r, int k, double p, double min_p, double u, 
 }
 
 // Draw without filters: the first id whose cumulated mass passes u times the
-// whole, from the groups' sums and one group's logits.
+// whole, from the groups' sums and one group's logits.  Each warp has a
+// contiguous share of the groups.
 __device__ int plain_draw(const Row& r, double u, SelectShared& s) {
-  const int lane = threadIdx.x & 31;
-  const int per = (r.n_grp + HS_THREADS - 1) / HS_THREADS;
-  const int ga = min(r.n_grp, (int)threadIdx.x * per), gb = min(r.n_grp, ga + per);
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int per = ((r.n_grp + HS_WARPS - 1) / HS_WARPS + 31) / 32 * 32;
+  const int ga = min(r.n_grp, w * per), gb = min(r.n_grp, ga + per);
   auto weight = [&](int g) {
-    return __ldg(r.gmass + (size_t)g * r.nt) * mass_of(r, key_value(grp_key(r, s, g)));
+    return g < gb ? __ldg(r.gmass + (size_t)g * r.nt) * mass_of(r, key_value(grp_key(r, s, g))) : 0.0;
   };
   double m = 0.0;
-  for (int g = ga; g < gb; ++g) m += weight(g);
-  double total;
-  const double before = block_scan(m, s, total);
+#pragma unroll 4
+  for (int g = ga + lane; g < gb; g += 32) m += weight(g);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+  __syncthreads();
+  if (lane == 0) s.red[w] = m;
+  __syncthreads();
+  double before = 0.0, total = 0.0;
+  int owner = 0;
+#pragma unroll
+  for (int i = 0; i < HS_WARPS; ++i) total += s.red[i];
   const double target = u * total;
-  // the thread whose share holds the target: the last that begins at or below it
-  const unsigned mine = m > 0.0 && before <= target ? threadIdx.x + 1u : 0u;
-  const unsigned owner = block_pick<true>(mine, s);
-  if (threadIdx.x + 1u == owner || (owner == 0u && threadIdx.x == 0)) {
-    double run = before;
-    int g = ga, best = ga;
-    double left = 0.0;
-    for (; g < gb; ++g) {
-      const double x = weight(g);
-      if (x > 0.0) {
-        best = g;
-        left = target - run;
-        if (run + x > target) break;
-      }
-      run += x;
+  // the warp whose share holds the target: the last that begins at or below it
+  double run = 0.0;
+  for (int i = 0; i < HS_WARPS; ++i) {
+    if (s.red[i] > 0.0 && run <= target) {
+      owner = i;
+      before = run;
     }
-    s.out_i = best;
-    s.out_d = left;
+    run += s.red[i];
   }
-  __syncthreads();
-  const int g = s.out_i;
-  const double left = s.out_d;
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    const int v = g * 32 + lane;
+  if (w == owner) {
+    double left = target - before;  // of the mass from group ga on
+    int best = ga;
+    double best_left = left;
+    for (int g0 = ga; g0 < gb; g0 += 32) {
+      const double own = weight(g0 + lane);
+      double inc = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const double x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+      }
+      const unsigned any = __ballot_sync(0xffffffffu, own > 0.0);
+      const unsigned over = __ballot_sync(0xffffffffu, own > 0.0 && inc > left);
+      if (any) {
+        // the first group that passes the target, else the last one so far
+        const int l = over ? __ffs((int)over) - 1 : 31 - __clz((int)any);
+        best = g0 + l;
+        best_left = left - __shfl_sync(0xffffffffu, inc - own, l);
+      }
+      if (over) break;
+      left -= __shfl_sync(0xffffffffu, inc, 31);
+    }
+    const int v = best * 32 + lane;
     const double own = v < r.V ? mass_of(r, __ldg(r.z + v)) : 0.0;
     double inc = own;
 #pragma unroll
@@ -650,9 +828,9 @@ __device__ int plain_draw(const Row& r, double u, SelectShared& s) {
       if (lane >= o) inc += x;
     }
     const unsigned any = __ballot_sync(0xffffffffu, own > 0.0);
-    const unsigned over = __ballot_sync(0xffffffffu, own > 0.0 && inc > left);
+    const unsigned over = __ballot_sync(0xffffffffu, own > 0.0 && inc > best_left);
     const int l = over ? __ffs((int)over) - 1 : 31 - __clz((int)any);
-    if (lane == 0) s.out_i = g * 32 + l;
+    if (lane == 0) s.out_i = best * 32 + l;
   }
   __syncthreads();
   return s.out_i;
@@ -683,6 +861,26 @@ __device__ int draw_from_candidates(const Row& r, int c, int k, double p, double
   // (both filters leave a prefix)
   const int n = (int)(block_sum((double)keep, s) + 0.5);
   if (n <= 1) return (int)(unsigned)s.cand[0];
+  if (n <= HS_THREADS) {
+    // each entry adds up the kept masses of the ids up to its own
+    const int i = threadIdx.x;
+    __syncthreads();
+    if (i < n) s.mass[i] = mass_of(r, key_value(cand_key(s.cand[i])));
+    __syncthreads();
+    const unsigned id = i < n ? (unsigned)s.cand[i] : 0u;
+    double cum = 0.0, sum = 0.0;
+    if ((i & ~31) < n)
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) {
+        const double x = s.mass[j];
+        sum += x;
+        cum += (unsigned)s.cand[j] <= id ? x : 0.0;
+      }
+    const bool live = i < n && s.mass[i] > 0.0;
+    const unsigned first = block_pick<false>(live && cum > u * sum ? id : 0x7fffffffu, s);
+    if (first != 0x7fffffffu) return (int)first;
+    return (int)block_pick<true>(live ? id : 0u, s);
+  }
   // the kept entries in the order of ids; their keys are needed for the masses
   __syncthreads();
   for (int i = threadIdx.x; i < n; i += HS_THREADS) {
@@ -711,7 +909,7 @@ __device__ int draw_from_candidates(const Row& r, int c, int k, double p, double
 }
 
 __device__ int sample_row(const Row& r, int k, double p, double min_p, double u, double total, bool greedy,
-                          unsigned top_key, SelectShared& s) {
+                          unsigned top_key, unsigned bottom_key, SelectShared& s) {
   if (k >= r.V || k < 0) k = 0;
   if (greedy || k == 1) {
     // the lowest id among the largest logits
@@ -727,7 +925,7 @@ __device__ int sample_row(const Row& r, int k, double p, double min_p, double u,
     return g * 32 + __ffs((int)eq) - 1;
   }
   if (k == 0 && p >= 1.0 && !(min_p > 0.0)) return plain_draw(r, u, s);
-  if (k > 0 && k <= kCap) return draw_from_candidates(r, top_candidates(r, k, s), k, p, min_p, u, total, s);
+  if (k > 0 && k <= kCap) return draw_from_candidates(r, top_candidates(r, k, top_key, bottom_key, s), k, p, min_p, u, total, s);
   if (k == 0) {
     // entries below min_p of the largest are out (a little slack: their own
     // masses decide); of the others, groups in growing numbers until their
@@ -739,9 +937,7 @@ __device__ int sample_row(const Row& r, int k, double p, double min_p, double u,
     }
     for (int want = 64; want <= 4096; want <<= 3) {
       unsigned thr = 0u;
-      int rank;
-      if (want < r.n_grp) thr = radix_select(r.n_grp, want, [&](int g) { return grp_key(r, s, g); }, s, rank);
-      if (p >= 1.0) thr = 0u;
+      if (want < r.n_grp && p < 1.0) thr = group_threshold(r, want, top_key, bottom_key, s);
       thr = max(thr, floor_key);
       const int c = gather_candidates(r, thr, s);
       if (c > kCap) break;
@@ -759,7 +955,7 @@ __device__ int sample_row(const Row& r, int k, double p, double min_p, double u,
 
 }  // namespace
 
-__global__ void __launch_bounds__(HS_THREADS) head_select_kernel(const HeadArgs a) {
+__global__ void __launch_bounds__(HS_THREADS, 1) head_select_kernel(const HeadArgs a) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   SelectShared& s = *reinterpret_cast<SelectShared*>(smem_raw);
   const int n = blockIdx.x;          // row of this chunk
@@ -774,13 +970,18 @@ __global__ void __launch_bounds__(HS_THREADS) head_select_kernel(const HeadArgs 
   r.nt = a.nt;
   r.scale = row_scale(a, row);
 
-  unsigned top = 0u;
+  r.tab = s.tab;
+  fill_exp_table(s.tab);
+  unsigned top = 0u, bottom = 0xffffffffu;
+#pragma unroll 8
   for (int g = threadIdx.x; g < r.n_grp; g += HS_THREADS) {
     const unsigned k = order_key(__ldg(r.gmax + (size_t)g * r.nt));
     if (g < kGrpCap) s.gkey[g] = k;
     top = max(top, k);
+    bottom = min(bottom, k);
   }
   top = block_pick<true>(top, s);
+  bottom = block_pick<false>(bottom, s);
   r.zmax = key_value(top);
   const bool timeout = (a.status[ST_FLAGS] & SF_TIMEOUT) != 0;
   const bool broken = top >= kKeyPosInf || top <= kKeyNegInf;  // an infinite (or NaN) logit on top
@@ -801,13 +1002,23 @@ __global__ void __launch_bounds__(HS_THREADS) head_select_kernel(const HeadArgs 
     return;
   }
   double m = 0.0;
-  for (int g = threadIdx.x; g < r.n_grp; g += HS_THREADS)
-    m += __ldg(r.gmass + (size_t)g * r.nt) * mass_of(r, key_value(grp_key(r, s, g)));
+  if (row_exact(a, row)) {
+#pragma unroll 8
+    for (int g = threadIdx.x; g < r.n_grp; g += HS_THREADS)
+      m += __ldg(r.gmass + (size_t)g * r.nt) * mass_of(r, key_value(grp_key(r, s, g)));
+  } else {
+    const float scale = (float)r.scale;
+    float mf = 0.f;
+#pragma unroll 8
+    for (int g = threadIdx.x; g < r.n_grp; g += HS_THREADS)
+      mf += (float)__ldg(r.gmass + (size_t)g * r.nt) * ex2_approx((key_value(grp_key(r, s, g)) - r.zmax) * scale);
+    m = (double)mf;
+  }
   const double total = block_sum(m, s);
   constexpr double kLn2 = 0.69314718055994530942;
 
   if (!a.u) {
-    const int c = top_candidates(r, a.k, s);
+    const int c = top_candidates(r, a.k, top, bottom, s);
     for (int i = threadIdx.x; i < a.k; i += HS_THREADS) {
       const unsigned long long cc = i < c ? s.cand[i] : 0ull;
       a.values[(size_t)row * a.k + i] = key_value(cand_key(cc));
@@ -824,22 +1035,25 @@ __global__ void __launch_bounds__(HS_THREADS) head_select_kernel(const HeadArgs 
   double min_p = (double)(a.min_p ? a.min_p[row] : a.min_p_all);
   min_p = min_p > 0.0 ? fmin(min_p, 1.0) : 0.0;
   const double u = fmax((double)a.u[row], 0.0);
-  const int token = sample_row(r, k, p, min_p, u, total, !(t > 0.f), top, s);
+  const int token = sample_row(r, k, p, min_p, u, total, !(t > 0.f), top, bottom, s);
   if (threadIdx.x == 0) {
     a.token[row] = token;
     a.logp[row] = (float)(((double)__ldg(r.z + token) - (double)r.zmax) * r.scale * kLn2 - log(total));
   }
 }
 
+// shared memory behind the stages: scales, table, row bits, barriers
+constexpr int kHeadExtra = HEAD_ROWS * 8 + kExpTab * 8 + 32 + 8 * (2 * HL_MAX_STAGES + 5) + 16;
+
 int head_logits_stages(int nt) {
-  const int fit = (227 * 1024 - 1024 - 2048 - 512) / (A_STAGE_BYTES + nt * 64);
+  const int fit = (227 * 1024 - 1024 - kHeadExtra) / (A_STAGE_BYTES + nt * 64);
   return fit < HL_MAX_STAGES ? fit : HL_MAX_STAGES;
 }
 
 // tmC: C in boxes of {64, 128}; tmE: E in boxes of {64, nt / 2}; grid: an even number of CTAs.
 cudaError_t launch_head_logits(const CUtensorMap& tmC, const CUtensorMap& tmE, const HeadArgs& a, int grid,
                                cudaStream_t stream) {
-  const size_t smem = 1024 + (size_t)a.stages * (A_STAGE_BYTES + a.nt * 64) + 2048 + 512;
+  const size_t smem = 1024 + (size_t)a.stages * (A_STAGE_BYTES + a.nt * 64) + kHeadExtra;
   cudaError_t e = cudaFuncSetAttribute(head_logits_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   head_logits_kernel<<<grid, HL_THREADS, smem, stream>>>(tmC, tmE, a);
