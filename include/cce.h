@@ -367,14 +367,14 @@ CCE_API cce_status_t cce_distill_backward(const void* E, const void* C, const in
                                           size_t workspace_bytes, void* stream);
 
 /* ---- Choosing among the head's logits ----
- * z_iv = E_i . C_v for 256 tokens at a time; nothing of size N x V is kept.
+ * z_iv = E_i . C_v for 512 tokens at a time; nothing of size N x V is kept.
  * -0 counts as +0; among equal logits the lowest id comes first.  A row whose
  * largest logit is infinite or NaN gets ids of -1 and NaN values, and sets
  * status flag bit 2; after a bounded wait that gave up (bit 0) every row of
  * the affected chunk does. */
 
 /* Workspace bytes of cce_top_logits and cce_sample (0 if the sizes are
- * invalid): the logits of min(N, 256) tokens in fp32 (262 MB at 256 tokens and
+ * invalid): the logits of min(N, 512) tokens in fp32 (524 MB at 512 tokens and
  * 256000 entries), 12 bytes per token and 32 vocabulary entries, and the
  * status block. */
 CCE_API size_t cce_head_workspace_size(int64_t N, int64_t D, int64_t V);

@@ -19,7 +19,7 @@ def top_logits(E, C, k: int, workspace: Optional[Workspace] = None, stream=None,
     lowest id first): values [N, k] fp32, ids [N, k] int64, and lse [N] fp32,
     the log-sum-exp over the vocabulary.  values and ids are what
     distill_forward takes of a teacher.  k is at most 1024 (and V).  The
-    scratch holds the logits of min(N, 256) tokens."""
+    scratch holds the logits of min(N, 512) tokens."""
     N, D, V = check_head(E, C)
     with Launch(E.device, stream, workspace) as run:
         if out is None:

@@ -48,8 +48,8 @@ cudaError_t launch_f32_to_bf16(const float* src, void* dst, size_t n, bool accum
 cudaError_t launch_distill_targets(const TargetArgs& a, cudaStream_t stream);
 cudaError_t launch_distill_finalize(const DistillFinArgs& a, cudaStream_t stream);
 int head_logits_stages(int nt);
-cudaError_t launch_head_logits(const CUtensorMap& tmC, const CUtensorMap& tmE, const HeadArgs& a, int grid,
-                               cudaStream_t stream);
+cudaError_t launch_head_logits(const CUtensorMap& tmC, const CUtensorMap& tmC32, const CUtensorMap& tmE,
+                               const HeadArgs& a, int grid, cudaStream_t stream);
 cudaError_t launch_head_select(const HeadArgs& a, cudaStream_t stream);
 }  // namespace cce
 
@@ -1225,35 +1225,33 @@ bool head_sizes_ok(int64_t N, int64_t D, int64_t V) {
   return sizes_ok(N, D, V) && V <= INT_MAX - 2 * BN;
 }
 
-// Workspace: status | a chunk's logits [rows][ld] fp32 | group sums [n_grp][nt]
-// fp64 | group maxima [n_grp][nt] fp32.
+// Workspace: status | a chunk's logits [rows][ld] fp32 | group sums
+// [rows][n_grp] fp64 | group maxima [rows][n_grp] fp32.
 struct HeadLayout {
-  int rows, nt, n_grp, ld;
+  int rows, n_grp, ld;
   size_t off_logits, off_mass, off_max, bytes;
 };
 
 HeadLayout plan_head(int64_t N, int64_t V) {
   HeadLayout L{};
   L.rows = (int)std::min<int64_t>(N, HEAD_ROWS);
-  L.nt = (L.rows + 31) / 32 * 32;  // (the pair's products take multiples of 32 columns)
   L.n_grp = (int)((V + 31) / 32);
   L.ld = L.n_grp * 32;
   L.off_logits = STATUS_BYTES;
   L.off_mass = L.off_logits + align_up((size_t)L.rows * L.ld * 4, 256);
-  L.off_max = L.off_mass + align_up((size_t)L.n_grp * L.nt * 8, 256);
-  L.bytes = L.off_max + align_up((size_t)L.n_grp * L.nt * 4, 256);
+  L.off_max = L.off_mass + align_up((size_t)L.rows * L.n_grp * 8, 256);
+  L.bytes = L.off_max + align_up((size_t)L.rows * L.n_grp * 4, 256);
   return L;
 }
 
 // Runs the chunks; a: settings and outputs.
 cce_status_t run_head(const void* E, const void* C, int64_t N, int64_t D, int64_t V, HeadArgs a, char* ws,
                       const HeadLayout& L, int sms, cudaStream_t stream) {
-  CUtensorMap tmC, tmE;
-  if (!make_map(&tmC, C, V, D, BM)) return CCE_ERR_CUDA;
+  CUtensorMap tmC, tmC32, tmE;
+  if (!make_map(&tmC, C, V, D, BM) || !make_map(&tmC32, C, V, D, 32)) return CCE_ERR_CUDA;
   if (cudaMemsetAsync(ws, 0, STATUS_BYTES, stream) != cudaSuccess) return CCE_ERR_CUDA;
   a.D = (int)D;
   a.V = (int)V;
-  a.n_vtile = (int)((V + BN - 1) / BN);
   a.n_grp = L.n_grp;
   a.ld = L.ld;
   a.logits = reinterpret_cast<float*>(ws + L.off_logits);
@@ -1262,16 +1260,21 @@ cce_status_t run_head(const void* E, const void* C, int64_t N, int64_t D, int64_
   a.status = reinterpret_cast<unsigned long long*>(ws);
   a.wait_limit_ns = g_wait_limit_ns.load();
   a.withhold_loads = g_withhold_loads.load();
-  const int grid = 2 * std::min(sms / 2, a.n_vtile);
+  // The vocabulary is shared out evenly: with tiles dealt whole, 594 tiles on
+  // 74 pairs take as long as 666.
+  const int pairs = sms / 2;
+  a.pair_rows = (a.n_grp + pairs - 1) / pairs * 32;
+  const int grid = 2 * ((a.n_grp * 32 + a.pair_rows - 1) / a.pair_rows);
   int box = 0;
   for (int64_t n0 = 0; n0 < N; n0 += HEAD_ROWS) {
     a.n0 = (int)n0;
     a.n_rows = (int)std::min<int64_t>(N - n0, HEAD_ROWS);
-    a.nt = (a.n_rows + 31) / 32 * 32;
+    a.n_blk = (a.n_rows + 255) / 256;
+    a.nt = ((a.n_rows + a.n_blk - 1) / a.n_blk + 31) / 32 * 32;  // (a pair's products take multiples of 32 columns)
     a.stages = head_logits_stages(a.nt);
     if (a.nt != box && !make_map(&tmE, E, N, D, a.nt / 2)) return CCE_ERR_CUDA;
     box = a.nt;
-    if (launch_head_logits(tmC, tmE, a, grid, stream) != cudaSuccess ||
+    if (launch_head_logits(tmC, tmC32, tmE, a, grid, stream) != cudaSuccess ||
         launch_head_select(a, stream) != cudaSuccess)
       return CCE_ERR_CUDA;
   }

@@ -126,17 +126,18 @@ struct DistillFinArgs {
 };
 
 // The head's logits of a chunk of tokens and the choice among them (head.cu).
-constexpr int HEAD_ROWS = 256;  // tokens per chunk
+constexpr int HEAD_ROWS = 512;  // tokens per chunk
 struct HeadArgs {
   int D, V;
   int n0, n_rows;      // the chunk's tokens: n0 .. n0 + n_rows - 1, n_rows <= HEAD_ROWS
-  int nt;              // n_rows rounded up to 32: the tiles' token side
-  int n_vtile, n_grp;  // 256-wide vocabulary tiles; groups of 32 entries
+  int n_blk, nt;       // blocks of tokens, and tokens of a block (a multiple of 32, at most 256)
+  int n_grp;           // groups of 32 vocabulary entries
+  int pair_rows;       // vocabulary entries of each CTA pair (a multiple of 32)
   int stages;
   int ld;              // floats from one token's logits to the next's
   float* logits;       // [n_rows][ld]
-  float* gmax;         // [n_grp][nt] largest logit of each group
-  double* gmass;       // [n_grp][nt] sum exp((z - gmax) / T)
+  float* gmax;         // [n_rows][n_grp] largest logit of each group
+  double* gmass;       // [n_rows][n_grp] sum exp((z - gmax) / T)
   unsigned long long* status;
   unsigned long long wait_limit_ns;
   int withhold_loads;

@@ -1,11 +1,14 @@
-// The head's logits of up to 256 tokens at a time, for choosing among them:
+// The head's logits of up to 512 tokens at a time, for choosing among them:
 // the k largest (top_logits) or one drawn token per row (sample).
 //
 //   z_iv = E_i . C_v;  x_iv = z_iv / T_i;
 //   log-probability of v: x_iv - log sum_w exp(x_iw)
 //
-// head_logits   C is read once per 256 tokens, which is what bounds the call
+// head_logits   C is read once per 512 tokens, which is what bounds the call
 //               below about 256 tokens (2 V D bytes); above, the products.
+//               (256 tokens at a time: 262 us for 256 tokens x 2304 x 256000,
+//               the time of 1.18 GB of C and 0.26 GB of logits; 512 at a time
+//               the products' time covers them.)
 //               The vocabulary is the M side of the tensor-core tiles and the
 //               tokens are the N side, so a batch of 16 multiplies 16 columns
 //               and not 256.  CTA pairs (cta_group::2): 256 vocabulary rows x
@@ -37,7 +40,7 @@ namespace cce {
 
 namespace {
 
-constexpr int HL_EPI_WARPS = 8;                  // two per TMEM lane group, alternate 32-token chunks
+constexpr int HL_EPI_WARPS = 16;                 // four per TMEM lane group, taking 32-token chunks in turn
 constexpr int HL_THREADS = 64 + 32 * HL_EPI_WARPS;
 constexpr int HL_MAX_STAGES = 12;
 constexpr double kLog2e = 1.4426950408889634074;
@@ -53,28 +56,29 @@ __device__ __forceinline__ float key_value(unsigned k) {
 constexpr unsigned kKeyPosInf = 0xff800000u;  // order_key(+inf)
 constexpr unsigned kKeyNegInf = 0x007fffffu;  // order_key(-inf)
 
-// 2^-t for t >= 0 (0 above 1000), off by a few units of 2^-53: t = k / 64 + r
-// with |r| <= 1 / 128, 2^-(k mod 64) / 64 from a table and 2^-r from its series
-// up to r^5 (the next term is below 4e-17).  About a third of the double
-// operations of a general exp2.
-constexpr int kExpTab = 64;
+// 2^-t for t >= 0, off by a few units of 2^-53: t = k / 1024 + r with
+// |r| <= 1 / 2048, 2^-(k / 1024) from a table (and the exponent) and 2^-r from
+// its series up to r^3 (the next term is below 6e-16).  A fraction of the
+// double operations of a general exp2.
+constexpr int kExpTab = 1024;
 __device__ __forceinline__ void fill_exp_table(double* tab) {
-  if (threadIdx.x < kExpTab) tab[threadIdx.x] = exp2(-(double)threadIdx.x / kExpTab);
+  for (int i = threadIdx.x; i < kExpTab; i += blockDim.x) tab[i] = exp2(-(double)i / kExpTab);
 }
-__device__ __forceinline__ double exp2_neg(double t, const double* tab) {
-  constexpr double kRound = 6755399441055744.0 / kExpTab;  // 1.5 2^52 / 64: adding it rounds to multiples of 1 / 64
+// 2^-t + add, for t <= 1000
+__device__ __forceinline__ double exp2_neg_plus(double t, double add, const double* tab) {
+  constexpr double kRound = 6755399441055744.0 / kExpTab;  // 1.5 2^52 / 1024: adding it rounds to multiples of 1 / 1024
   const double u = t + kRound;
   const int k = __double2loint(u);
   const double r = t - (u - kRound);
   // (-ln 2)^n / n!
-  double q = fma(r, -1.3333558146428443e-3, 9.6181291076284772e-3);
-  q = fma(q, r, -5.5504108664821580e-2);
-  q = fma(q, r, 2.4022650695910071e-1);
+  double q = fma(r, -5.5504108664821580e-2, 2.4022650695910071e-1);
   q = fma(q, r, -6.9314718055994531e-1);
   q = fma(q, r, 1.0);
-  q *= tab[k & (kExpTab - 1)];
-  const double e = __hiloint2double(__double2hiint(q) - ((k >> 6) << 20), __double2loint(q));
-  return t < 1000.0 ? e : 0.0;
+  const double w = tab[k & (kExpTab - 1)];
+  return fma(q, __hiloint2double(__double2hiint(w) - ((k >> 10) << 20), __double2loint(w)), add);
+}
+__device__ __forceinline__ double exp2_neg(double t, const double* tab) {
+  return t < 1000.0 ? exp2_neg_plus(t, 0.0, tab) : 0.0;
 }
 
 // Whether a row's token hangs on sums over the whole vocabulary: a draw
@@ -103,15 +107,16 @@ __device__ __forceinline__ double row_scale(const HeadArgs& a, int n) {
 }  // namespace
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(HL_THREADS, 1)
-    head_logits_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmE,
-                       const HeadArgs a) {
+    head_logits_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmC32,
+                       const __grid_constant__ CUtensorMap tmE, const HeadArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int S = a.stages;
   const uint32_t stage_bytes = (uint32_t)(A_STAGE_BYTES + a.nt * 64);  // [128 voc][64 d] and [nt / 2 tok][64 d]
-  double* scale = reinterpret_cast<double*>(smem + (size_t)S * stage_bytes);  // [256] log2(e) / T
-  double* tab = scale + HEAD_ROWS;
-  unsigned* exact = reinterpret_cast<unsigned*>(tab + kExpTab);               // [8] a bit per row: row_exact
+  double* tab = reinterpret_cast<double*>(smem + (size_t)S * stage_bytes);
+  double* scale = tab + kExpTab;                                          // [HEAD_ROWS] log2(e) / T
+  float* scale_f = reinterpret_cast<float*>(scale + HEAD_ROWS);           // [HEAD_ROWS]
+  unsigned* exact = reinterpret_cast<unsigned*>(scale_f + HEAD_ROWS);     // a bit per row: row_exact
   uint64_t* bars = reinterpret_cast<uint64_t*>(exact + HEAD_ROWS / 32);
   uint64_t* full = bars;                    // leader: both CTAs' copies landed
   uint64_t* empty = full + HL_MAX_STAGES;   // each CTA: stage free again
@@ -125,8 +130,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(HL_THREADS, 1)
   const int lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
-  const int pair = blockIdx.x >> 1;
-  const int n_pairs = gridDim.x >> 1;
+  // this pair's vocabulary entries: whole groups, as many for every pair as
+  // can be; the last tile is loaded as far as it reaches
+  const int va = min(a.V, (blockIdx.x >> 1) * a.pair_rows), vb = min(a.V, va + a.pair_rows);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -147,14 +153,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(HL_THREADS, 1)
   }
   if (threadIdx.x == 32) {
     tma_prefetch_map(&tmC);
+    tma_prefetch_map(&tmC32);
     tma_prefetch_map(&tmE);
   }
-  if (threadIdx.x < HEAD_ROWS) {  // (whole warps)
-    const int n = threadIdx.x;
+  for (int n = threadIdx.x; n < HEAD_ROWS; n += HL_THREADS) {  // (whole warps)
     const bool live = n < a.n_rows;
     scale[n] = live ? row_scale(a, a.n0 + n) : 1.0;
+    scale_f[n] = (float)scale[n];
     const unsigned bits = __ballot_sync(0xffffffffu, live && row_exact(a, a.n0 + n));
-    if (lane == 0) exact[warp] = bits;
+    if (lane == 0) exact[n >> 5] = bits;
   }
   fill_exp_table(tab);
   tc_fence_before();
@@ -169,17 +176,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(HL_THREADS, 1)
       // ---------------- TMA producer (both CTAs) ----------------
       int stage = 0;
       uint32_t phase = 0, armed = 0;
-      for (int vt = a.withhold_loads ? a.n_vtile : pair; vt < a.n_vtile; vt += n_pairs) {
-        for (int kb = 0; kb < nkb; ++kb) {
-          if (!mbar_wait(&empty[stage], phase ^ 1u, wc)) goto producer_done;
-          uint8_t* X = smem + (size_t)stage * stage_bytes;
-          if (leader) mbar_arrive_expect_tx(&full[stage], 2u * stage_bytes);
-          tma_load_2d_pair(X, &tmC, &full[stage], kb * BK, vt * BN + (int)rank * BM);
-          tma_load_2d_pair(X + A_STAGE_BYTES, &tmE, &full[stage], kb * BK, a.n0 + (int)rank * (a.nt / 2));
-          armed |= 1u << stage;
-          if (++stage == S) {
-            stage = 0;
-            phase ^= 1u;
+      for (int v0 = a.withhold_loads ? vb : va; v0 < vb; v0 += BN) {
+        // groups of this tile (of 8), and of this CTA's half of it
+        const int groups = min(BN / 32, (vb - v0 + 31) / 32);
+        const int mine = min(BM / 32, max(0, groups - (int)rank * (BM / 32)));
+        const uint32_t bytes = (uint32_t)(groups * 32 * BK * 2 + 2 * a.nt * 64);
+        const int y = v0 + (int)rank * BM;
+        // (a second block of tokens finds the tile's rows of C in L2)
+        for (int blk = 0; blk < a.n_blk; ++blk) {
+          for (int kb = 0; kb < nkb; ++kb) {
+            if (!mbar_wait(&empty[stage], phase ^ 1u, wc)) goto producer_done;
+            uint8_t* X = smem + (size_t)stage * stage_bytes;
+            if (leader) mbar_arrive_expect_tx(&full[stage], bytes);
+            if (mine == BM / 32)
+              tma_load_2d_pair(X, &tmC, &full[stage], kb * BK, y);
+            else  // (what the other rows of the stage hold only reaches logits that nobody reads)
+              for (int g = 0; g < mine; ++g)
+                tma_load_2d_pair(X + g * 4096, &tmC32, &full[stage], kb * BK, y + g * 32);
+            tma_load_2d_pair(X + A_STAGE_BYTES, &tmE, &full[stage], kb * BK,
+                             a.n0 + blk * a.nt + (int)rank * (a.nt / 2));
+            armed |= 1u << stage;
+            if (++stage == S) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
         }
       }
@@ -197,7 +217,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(HL_THREADS, 1)
       const uint32_t idesc = idesc_bf16_f32(2 * BM, a.nt, false, false);
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
-      for (int vt = pair; vt < a.n_vtile; vt += n_pairs) {
+      for (int t = 0; t < a.n_blk * ((vb - va + BN - 1) / BN); ++t) {
         if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, wc)) goto mma_done;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(acc * 256);
@@ -237,24 +257,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(HL_THREADS, 1)
     const uint32_t lane_addr = (uint32_t)(lg * 32) << 16;
     const uint32_t tempty_leader0 = mapa_shared(smem_u32(&tempty[0]), 0);
     const uint32_t tempty_leader1 = mapa_shared(smem_u32(&tempty[1]), 0);
-    const int n_chunk = (a.n_rows + 31) / 32;
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int vt = pair; vt < a.n_vtile; vt += n_pairs) {
+    for (int t = 0; t < a.n_blk * ((vb - va + BN - 1) / BN); ++t) {
+      const int v0 = va + t / a.n_blk * BN, row0 = t % a.n_blk * a.nt;  // first row of the block of tokens
+      const int n_chunk = (min(a.nt, a.n_rows - row0) + 31) / 32;
       const bool ready = __all_sync(0xffffffffu, mbar_wait(&tfull[acc], acc_phase, wc));
       if (!ready) break;
       tc_fence_after();
-      const int v = vt * BN + (int)rank * BM + lg * 32 + lane;
+      const int v = v0 + (int)rank * BM + lg * 32 + lane;
       const int grp = v >> 5;
-      const bool in = v < a.V;
-      for (int c = hsel; c < n_chunk; c += 2) {
+      const bool in = v < vb;
+      for (int c = hsel; c < n_chunk && v - lane < vb; c += HL_EPI_WARPS / 4) {
         float x[32];
         tmem_ld32(tmem_base + lane_addr + (uint32_t)(acc * 256 + c * 32), x);
-        const int n_here = min(32, a.n_rows - c * 32);
-        float* dst = a.logits + (size_t)(c * 32) * a.ld + v;
-        const bool in_double = exact[c] != 0u;  // (for the whole chunk)
+        const int row = row0 + c * 32;  // of the chunk's first token (a multiple of 32)
+        const int n_here = min(32, a.n_rows - row);
+        float* dst = a.logits + (size_t)row * a.ld + v;
+        const bool in_double = exact[row >> 5] != 0u;  // (for all of the 32)
+        // lane j keeps column j's maximum and sum
         float my_max = 0.f;
-        double my_mass = 0.0;
+        unsigned my_hi = 0u, my_lo = 0u;
 #pragma unroll
         for (int j0 = 0; j0 < 32; j0 += 8) {
           if (j0 < n_here) {
@@ -276,32 +299,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(HL_THREADS, 1)
             if (!in_double) {
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
-                const float e = ex2_approx((x[j0 + j] - m[j]) * (float)scale[c * 32 + j0 + j]);
+                const float e = ex2_approx((x[j0 + j] - m[j]) * scale_f[row + j0 + j]);
                 const unsigned sum = __reduce_add_sync(0xffffffffu, __float2uint_rn(e * 67108864.f));
-                if (lane == j0 + j) {
-                  my_max = m[j];
-                  my_mass = (double)sum * (1.0 / 67108864.0);
-                }
+                my_max = lane == j0 + j ? m[j] : my_max;
+                my_hi = lane == j0 + j ? sum : my_hi;
               }
             } else {
+              // (m widened by the lane of its column; terms below 2^-80 of the
+              // largest round to nothing)
+#pragma unroll
+              for (int j = 0; j < 8; ++j) my_max = lane == j0 + j ? m[j] : my_max;
+              const double mine = (double)my_max;
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
-                const double t = ((double)m[j] - (double)x[j0 + j]) * scale[c * 32 + j0 + j];
-                const double w = exp2_neg(t, tab) + 2.0;  // in [2, 3]: the fraction's 52 bits are e in units of 2^-51
+                const double wide_m = __shfl_sync(0xffffffffu, mine, j0 + j);
+                double t = (wide_m - (double)x[j0 + j]) * scale[row + j0 + j];
+                t = __hiloint2double(min(__double2hiint(t), 0x40540000), __double2loint(t));  // at most about 80
+                const double w = exp2_neg_plus(t, 2.0, tab);  // in [2, 3]: the fraction's 52 bits are e in units of 2^-51
                 const unsigned whi = (unsigned)__double2hiint(w) & 0xfffffu, wlo = (unsigned)__double2loint(w);
                 const unsigned hi = __reduce_add_sync(0xffffffffu, (whi << 6) | (wlo >> 26));
                 const unsigned lo = __reduce_add_sync(0xffffffffu, wlo & 0x3ffffffu);
-                if (lane == j0 + j) {
-                  my_max = m[j];
-                  my_mass = ((double)hi * 67108864.0 + (double)lo) * (1.0 / 2251799813685248.0);
-                }
+                my_hi = lane == j0 + j ? hi : my_hi;
+                my_lo = lane == j0 + j ? lo : my_lo;
               }
             }
           }
         }
-        if (lane < n_here && grp < a.n_grp) {
-          a.gmax[(size_t)grp * a.nt + c * 32 + lane] = my_max;
-          a.gmass[(size_t)grp * a.nt + c * 32 + lane] = my_mass;
+        if (lane < n_here) {
+          // (the eight groups of a tile fill whole sectors of each token's list)
+          const size_t at = (size_t)(row + lane) * a.n_grp + grp;
+          a.gmax[at] = my_max;
+          a.gmass[at] = in_double ? ((double)my_hi * 67108864.0 + (double)my_lo) * (1.0 / 2251799813685248.0)
+                                  : (double)my_hi * (1.0 / 67108864.0);
         }
       }
       tc_fence_before();
@@ -343,30 +372,43 @@ struct SelectShared {
     int list[2 * kCap];           // groups to read
   };
   double tab[kExpTab];
-  double red[HS_WARPS + 1];
+  double red[HS_WARPS];
   unsigned hist[256];
   unsigned ured[3][HS_WARPS];
+  int rank[HS_THREADS];
   int count;
   unsigned found_key;
   int found_rank;
   int out_i;
-  double out_d;
   unsigned gkey[kGrpCap];
 };
 
 // A row's view of head_logits' results.
 struct Row {
   const float* z;       // [V]
-  const float* gmax;    // [n_grp], stride nt
-  const double* gmass;  // [n_grp], stride nt
-  int V, n_grp, nt;
+  const float* gmax;    // [n_grp]
+  const double* gmass;  // [n_grp]
+  int V, n_grp;
   float zmax;
   double scale;         // log2(e) / T
   const double* tab;
 };
 
+// f(group, value) for this thread's groups, eight loads at a time.
+template <typename T, typename F>
+__device__ __forceinline__ void each_group(const T* __restrict__ p, int n, F f) {
+  for (int g0 = threadIdx.x; g0 < n; g0 += 8 * HS_THREADS) {
+    T v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = g0 + j * HS_THREADS < n ? __ldg(p + g0 + j * HS_THREADS) : T(0);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (g0 + j * HS_THREADS < n) f(g0 + j * HS_THREADS, v[j]);
+  }
+}
+
 __device__ __forceinline__ unsigned grp_key(const Row& r, const SelectShared& s, int g) {
-  return g < kGrpCap ? s.gkey[g] : order_key(__ldg(r.gmax + (size_t)g * r.nt));
+  return g < kGrpCap ? s.gkey[g] : order_key(__ldg(r.gmax + g));
 }
 // exp((z - zmax) / T)
 __device__ __forceinline__ double mass_of(const Row& r, float z) {
@@ -379,10 +421,11 @@ __device__ __forceinline__ double block_sum(double v, SelectShared& s) {
   __syncthreads();
   if ((threadIdx.x & 31) == 0) s.red[threadIdx.x >> 5] = v;
   __syncthreads();
-  double t = 0.0;
+  // every warp adds the warps' sums in the same tree
+  v = s.red[threadIdx.x & (HS_WARPS - 1)];
 #pragma unroll
-  for (int i = 0; i < HS_WARPS; ++i) t += s.red[i];
-  return t;
+  for (int o = HS_WARPS / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
 }
 template <bool MAX>
 __device__ __forceinline__ unsigned block_pick(unsigned v, SelectShared& s) {
@@ -390,10 +433,8 @@ __device__ __forceinline__ unsigned block_pick(unsigned v, SelectShared& s) {
   __syncthreads();
   if ((threadIdx.x & 31) == 0) s.ured[0][threadIdx.x >> 5] = v;
   __syncthreads();
-  unsigned t = s.ured[0][0];
-#pragma unroll
-  for (int i = 1; i < HS_WARPS; ++i) t = MAX ? max(t, s.ured[0][i]) : min(t, s.ured[0][i]);
-  return t;
+  v = s.ured[0][threadIdx.x & (HS_WARPS - 1)];
+  return MAX ? __reduce_max_sync(0xffffffffu, v) : __reduce_min_sync(0xffffffffu, v);
 }
 // Exclusive prefix sum of one double per thread; total to every thread.
 __device__ __forceinline__ double block_scan(double v, SelectShared& s, double& total) {
@@ -465,18 +506,38 @@ __device__ unsigned radix_select(int n, int want, KeyFn key, SelectShared& s, in
 }
 
 // A key that at least `want` group maxima reach (1 <= want <= n_grp), and not
-// many more: three counts a pass split the keys between one that is reached
-// often enough and one that is not into four, until the number is within half
-// of `want` or the keys are exhausted.  (A radix select's first digits put
-// every group into one bin: 8000 additions to one word a digit, 76 us a row.)
-__device__ unsigned group_threshold(const Row& r, int want, unsigned top, unsigned bottom, SelectShared& s) {
+// many more.  mine: the largest key of this thread's groups.  For few, the
+// threads' largest keys stand for all groups (the want-th largest of 512 bins'
+// maxima is a bound too, and seldom a lower one) and are halved by counting
+// threads; else three counts a pass over all groups split the keys between one
+// that is reached often enough and one that is not into four.  Either ends when
+// the number is within half of `want` or the keys are exhausted.  (A radix
+// select's first digits put every group into one bin: 8000 additions to one
+// word a digit, and 77 us for one row of 256000 entries.)
+__device__ unsigned group_threshold(const Row& r, int want, unsigned mine, unsigned top, unsigned bottom,
+                                    SelectShared& s) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   unsigned lo = bottom, hi = top + 1u;  // count(>= lo) >= want > count(>= hi)
   const int enough = want + want / 2 + 16;
+  if (want <= HS_THREADS / 4 && r.n_grp >= HS_THREADS) {
+    lo = block_pick<false>(mine, s);
+    while (hi - lo > 1u) {
+      const unsigned mid = lo + (hi - lo) / 2u;
+      const int c = __syncthreads_count(mine >= mid);
+      if (c >= want) {
+        lo = mid;
+        if (c <= enough) break;
+      } else {
+        hi = mid;
+      }
+    }
+    return lo;
+  }
   while (hi - lo > 1u) {
     const unsigned step = max(1u, (hi - lo) / 4u);
     const unsigned t1 = lo + step, t2 = min(hi, t1 + step), t3 = min(hi, t2 + step);
     unsigned c1 = 0u, c2 = 0u, c3 = 0u;
+#pragma unroll 4
     for (int g = threadIdx.x; g < r.n_grp; g += HS_THREADS) {
       const unsigned k = grp_key(r, s, g);
       c1 += k >= t1;
@@ -493,13 +554,10 @@ __device__ unsigned group_threshold(const Row& r, int want, unsigned top, unsign
       s.ured[2][w] = c3;
     }
     __syncthreads();
-    c1 = c2 = c3 = 0u;
-#pragma unroll
-    for (int i = 0; i < HS_WARPS; ++i) {
-      c1 += s.ured[0][i];
-      c2 += s.ured[1][i];
-      c3 += s.ured[2][i];
-    }
+    const unsigned half = lane < HS_WARPS ? 1u : 0u;
+    c1 = __reduce_add_sync(0xffffffffu, half * s.ured[0][lane & (HS_WARPS - 1)]);
+    c2 = __reduce_add_sync(0xffffffffu, half * s.ured[1][lane & (HS_WARPS - 1)]);
+    c3 = __reduce_add_sync(0xffffffffu, half * s.ured[2][lane & (HS_WARPS - 1)]);
     int c_lo = INT_MAX;
     if ((int)c3 >= want) {
       lo = t3;
@@ -530,6 +588,7 @@ __device__ int gather_candidates(const Row& r, unsigned thr, SelectShared& s) {
     s.found_rank = 0;
   }
   __syncthreads();
+#pragma unroll 4
   for (int g = threadIdx.x; g < r.n_grp; g += HS_THREADS)
     if (grp_key(r, s, g) >= thr) {
       const int at = atomicAdd(&s.found_rank, 1);
@@ -564,22 +623,37 @@ __device__ int gather_candidates(const Row& r, unsigned thr, SelectShared& s) {
   return s.count;
 }
 
+// How many of n <= HS_THREADS entries are below this thread's (threads 0 .. n - 1
+// hold one each): below(j) tells whether entry j is.  The comparisons of an
+// entry are shared by HS_THREADS / n threads.
+template <typename Fn>
+__device__ int block_rank(int n, Fn below, SelectShared& s) {
+  int m = 32;
+  while (m < n) m <<= 1;
+  const int i = threadIdx.x & (m - 1), parts = HS_THREADS / m, part = threadIdx.x / m;
+  __syncthreads();
+  s.rank[threadIdx.x] = 0;
+  __syncthreads();
+  int c = 0;
+  if (i < n)
+#pragma unroll 4
+    for (int j = part; j < n; j += parts) c += below(i, j);
+  if (c) atomicAdd(&s.rank[i], c);
+  __syncthreads();
+  return s.rank[threadIdx.x];
+}
+
 // Sorts s.cand[0 .. n) ascending (n <= kCap; the rest up to a power of two is filled).
 __device__ void sort_candidates(SelectShared& s, int n) {
-  __syncthreads();
   if (n <= HS_THREADS) {
-    // every entry counts the smaller ones (all differ): no steps to wait for
-    const int i = threadIdx.x;
-    const unsigned long long mine = i < n ? s.cand[i] : 0ull;
-    int rank = 0;
-    if ((i & ~31) < n)
-#pragma unroll 4
-      for (int j = 0; j < n; ++j) rank += s.cand[j] < mine;
+    const int rank = block_rank(n, [&](int i, int j) { return (int)(s.cand[j] < s.cand[i]); }, s);
+    const unsigned long long mine = (int)threadIdx.x < n ? s.cand[threadIdx.x] : 0ull;
     __syncthreads();
-    if (i < n) s.cand[rank] = mine;
+    if ((int)threadIdx.x < n) s.cand[rank] = mine;
     __syncthreads();
     return;
   }
+  __syncthreads();
   int size2 = 1;
   while (size2 < n) size2 <<= 1;
   __syncthreads();
@@ -642,10 +716,10 @@ __device__ int gather_exact(const Row& r, unsigned kappa, int ties, SelectShared
 
 // The k largest entries (k <= kCap, k <= V) as candidates: at least these,
 // sorted; their number.
-__device__ int top_candidates(const Row& r, int k, unsigned top, unsigned bottom, SelectShared& s) {
+__device__ int top_candidates(const Row& r, int k, unsigned mine, unsigned top, unsigned bottom, SelectShared& s) {
   int c = kCap + 1, rank;
   if (r.n_grp >= k)
-    c = gather_candidates(r, group_threshold(r, k, top, bottom, s), s);
+    c = gather_candidates(r, group_threshold(r, k, mine, top, bottom, s), s);
   else if (r.V <= kCap)
     c = gather_candidates(r, 0u, s);
   if (c > kCap) {
@@ -767,24 +841,24 @@ __device__ int wide_draw(const Row& r, int k, double p, double min_p, double u, 
 // Draw without filters: the first id whose cumulated mass passes u times the
 // whole, from the groups' sums and one group's logits.  Each warp has a
 // contiguous share of the groups.
-__device__ int plain_draw(const Row& r, double u, SelectShared& s) {
+__device__ int plain_draw(const Row& r, double u, SelectShared& s, double& total) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int per = ((r.n_grp + HS_WARPS - 1) / HS_WARPS + 31) / 32 * 32;
   const int ga = min(r.n_grp, w * per), gb = min(r.n_grp, ga + per);
   auto weight = [&](int g) {
-    return g < gb ? __ldg(r.gmass + (size_t)g * r.nt) * mass_of(r, key_value(grp_key(r, s, g))) : 0.0;
+    return g < gb ? __ldg(r.gmass + g) * mass_of(r, key_value(grp_key(r, s, g))) : 0.0;
   };
   double m = 0.0;
-#pragma unroll 4
+#pragma unroll 8
   for (int g = ga + lane; g < gb; g += 32) m += weight(g);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
   __syncthreads();
   if (lane == 0) s.red[w] = m;
   __syncthreads();
-  double before = 0.0, total = 0.0;
+  double before = 0.0;
   int owner = 0;
-#pragma unroll
+  total = 0.0;
   for (int i = 0; i < HS_WARPS; ++i) total += s.red[i];
   const double target = u * total;
   // the warp whose share holds the target: the last that begins at or below it
@@ -840,6 +914,28 @@ __device__ int plain_draw(const Row& r, double u, SelectShared& s) {
 __device__ int draw_from_candidates(const Row& r, int c, int k, double p, double min_p, double u, double total,
                                     SelectShared& s) {
   if (k > 0) c = min(c, k);
+  if (c <= HS_THREADS) {
+    // an entry per thread
+    const int i = threadIdx.x;
+    const unsigned long long mine = i < c ? s.cand[i] : 0ull;
+    double e = i < c ? mass_of(r, key_value(cand_key(mine))) : 0.0, sum;
+    const double before = block_scan(e, s, sum);
+    if (k > 0) total = sum;
+    // (both filters leave a prefix)
+    const int n = __syncthreads_count(i < c && (i == 0 || p >= 1.0 || before < p * total) && e >= min_p);
+    if (n <= 1) return (int)(unsigned)s.cand[0];
+    const int rank = block_rank(n, [&](int x, int y) { return (int)((unsigned)s.cand[y] < (unsigned)s.cand[x]); }, s);
+    if (i < n) {
+      s.cand[rank] = mine & 0xffffffffull;
+      s.mass[rank] = e;
+    }
+    __syncthreads();
+    e = i < n ? s.mass[i] : 0.0;
+    const double cum = block_scan(e, s, sum) + e;
+    unsigned first = block_pick<false>(e > 0.0 && cum > u * sum ? (unsigned)i : 0x7fffffffu, s);
+    if (first == 0x7fffffffu) first = block_pick<true>(e > 0.0 ? (unsigned)i : 0u, s);
+    return (int)s.cand[first];
+  }
   constexpr int PER = kCap / HS_THREADS;
   // masses in falling order and what comes before each
   const int i0 = threadIdx.x * PER;
@@ -861,26 +957,6 @@ __device__ int draw_from_candidates(const Row& r, int c, int k, double p, double
   // (both filters leave a prefix)
   const int n = (int)(block_sum((double)keep, s) + 0.5);
   if (n <= 1) return (int)(unsigned)s.cand[0];
-  if (n <= HS_THREADS) {
-    // each entry adds up the kept masses of the ids up to its own
-    const int i = threadIdx.x;
-    __syncthreads();
-    if (i < n) s.mass[i] = mass_of(r, key_value(cand_key(s.cand[i])));
-    __syncthreads();
-    const unsigned id = i < n ? (unsigned)s.cand[i] : 0u;
-    double cum = 0.0, sum = 0.0;
-    if ((i & ~31) < n)
-#pragma unroll 4
-      for (int j = 0; j < n; ++j) {
-        const double x = s.mass[j];
-        sum += x;
-        cum += (unsigned)s.cand[j] <= id ? x : 0.0;
-      }
-    const bool live = i < n && s.mass[i] > 0.0;
-    const unsigned first = block_pick<false>(live && cum > u * sum ? id : 0x7fffffffu, s);
-    if (first != 0x7fffffffu) return (int)first;
-    return (int)block_pick<true>(live ? id : 0u, s);
-  }
   // the kept entries in the order of ids; their keys are needed for the masses
   __syncthreads();
   for (int i = threadIdx.x; i < n; i += HS_THREADS) {
@@ -908,8 +984,8 @@ __device__ int draw_from_candidates(const Row& r, int c, int k, double p, double
   return (int)(s.cand[pick] >> 32);
 }
 
-__device__ int sample_row(const Row& r, int k, double p, double min_p, double u, double total, bool greedy,
-                          unsigned top_key, unsigned bottom_key, SelectShared& s) {
+__device__ int sample_row(const Row& r, int k, double p, double min_p, double u, double& total, bool greedy,
+                          unsigned mine, unsigned top_key, unsigned bottom_key, SelectShared& s) {
   if (k >= r.V || k < 0) k = 0;
   if (greedy || k == 1) {
     // the lowest id among the largest logits
@@ -924,8 +1000,8 @@ __device__ int sample_row(const Row& r, int k, double p, double min_p, double u,
     const unsigned eq = __ballot_sync(0xffffffffu, v < r.V && order_key(__ldg(r.z + v)) == top_key);
     return g * 32 + __ffs((int)eq) - 1;
   }
-  if (k == 0 && p >= 1.0 && !(min_p > 0.0)) return plain_draw(r, u, s);
-  if (k > 0 && k <= kCap) return draw_from_candidates(r, top_candidates(r, k, top_key, bottom_key, s), k, p, min_p, u, total, s);
+  if (k == 0 && p >= 1.0 && !(min_p > 0.0)) return plain_draw(r, u, s, total);
+  if (k > 0 && k <= kCap) return draw_from_candidates(r, top_candidates(r, k, mine, top_key, bottom_key, s), k, p, min_p, u, total, s);
   if (k == 0) {
     // entries below min_p of the largest are out (a little slack: their own
     // masses decide); of the others, groups in growing numbers until their
@@ -937,7 +1013,7 @@ __device__ int sample_row(const Row& r, int k, double p, double min_p, double u,
     }
     for (int want = 64; want <= 4096; want <<= 3) {
       unsigned thr = 0u;
-      if (want < r.n_grp && p < 1.0) thr = group_threshold(r, want, top_key, bottom_key, s);
+      if (want < r.n_grp && p < 1.0) thr = group_threshold(r, want, mine, top_key, bottom_key, s);
       thr = max(thr, floor_key);
       const int c = gather_candidates(r, thr, s);
       if (c > kCap) break;
@@ -963,24 +1039,22 @@ __global__ void __launch_bounds__(HS_THREADS, 1) head_select_kernel(const HeadAr
   const float qnan = __int_as_float(0x7fc00000);
   Row r;
   r.z = a.logits + (size_t)n * a.ld;
-  r.gmax = a.gmax + n;
-  r.gmass = a.gmass + n;
+  r.gmax = a.gmax + (size_t)n * a.n_grp;
+  r.gmass = a.gmass + (size_t)n * a.n_grp;
   r.V = a.V;
   r.n_grp = a.n_grp;
-  r.nt = a.nt;
   r.scale = row_scale(a, row);
 
   r.tab = s.tab;
   fill_exp_table(s.tab);
-  unsigned top = 0u, bottom = 0xffffffffu;
-#pragma unroll 8
-  for (int g = threadIdx.x; g < r.n_grp; g += HS_THREADS) {
-    const unsigned k = order_key(__ldg(r.gmax + (size_t)g * r.nt));
+  unsigned mine = 0u, bottom = 0xffffffffu;
+  each_group(r.gmax, r.n_grp, [&](int g, float v) {
+    const unsigned k = order_key(v);
     if (g < kGrpCap) s.gkey[g] = k;
-    top = max(top, k);
+    mine = max(mine, k);
     bottom = min(bottom, k);
-  }
-  top = block_pick<true>(top, s);
+  });
+  const unsigned top = block_pick<true>(mine, s);
   bottom = block_pick<false>(bottom, s);
   r.zmax = key_value(top);
   const bool timeout = (a.status[ST_FLAGS] & SF_TIMEOUT) != 0;
@@ -1001,24 +1075,29 @@ __global__ void __launch_bounds__(HS_THREADS, 1) head_select_kernel(const HeadAr
     }
     return;
   }
-  double m = 0.0;
-  if (row_exact(a, row)) {
-#pragma unroll 8
-    for (int g = threadIdx.x; g < r.n_grp; g += HS_THREADS)
-      m += __ldg(r.gmass + (size_t)g * r.nt) * mass_of(r, key_value(grp_key(r, s, g)));
-  } else {
-    const float scale = (float)r.scale;
-    float mf = 0.f;
-#pragma unroll 8
-    for (int g = threadIdx.x; g < r.n_grp; g += HS_THREADS)
-      mf += (float)__ldg(r.gmass + (size_t)g * r.nt) * ex2_approx((key_value(grp_key(r, s, g)) - r.zmax) * scale);
-    m = (double)mf;
+  // sum exp((z - zmax) / T): in double where the token hangs on it (a draw
+  // without filters forms it on its way)
+  const bool exact = row_exact(a, row);
+  const bool plain = exact && !((a.top_p ? a.top_p[row] : a.top_p_all) < 1.f);
+  double total = 0.0;
+  if (!plain) {
+    double m = 0.0;
+    if (exact) {
+      each_group(r.gmass, r.n_grp, [&](int g, double v) { m += v * mass_of(r, key_value(grp_key(r, s, g))); });
+    } else {
+      const float scale = (float)r.scale;
+      float mf = 0.f;
+      each_group(r.gmass, r.n_grp, [&](int g, double v) {
+        mf += (float)v * ex2_approx((key_value(grp_key(r, s, g)) - r.zmax) * scale);
+      });
+      m = (double)mf;
+    }
+    total = block_sum(m, s);
   }
-  const double total = block_sum(m, s);
   constexpr double kLn2 = 0.69314718055994530942;
 
   if (!a.u) {
-    const int c = top_candidates(r, a.k, top, bottom, s);
+    const int c = top_candidates(r, a.k, mine, top, bottom, s);
     for (int i = threadIdx.x; i < a.k; i += HS_THREADS) {
       const unsigned long long cc = i < c ? s.cand[i] : 0ull;
       a.values[(size_t)row * a.k + i] = key_value(cand_key(cc));
@@ -1035,28 +1114,29 @@ __global__ void __launch_bounds__(HS_THREADS, 1) head_select_kernel(const HeadAr
   double min_p = (double)(a.min_p ? a.min_p[row] : a.min_p_all);
   min_p = min_p > 0.0 ? fmin(min_p, 1.0) : 0.0;
   const double u = fmax((double)a.u[row], 0.0);
-  const int token = sample_row(r, k, p, min_p, u, total, !(t > 0.f), top, bottom, s);
+  int token = sample_row(r, k, p, min_p, u, total, !(t > 0.f), mine, top, bottom, s);
   if (threadIdx.x == 0) {
+    token = min(max(token, 0), a.V - 1);  // (an index into the row whatever the workspace holds)
     a.token[row] = token;
     a.logp[row] = (float)(((double)__ldg(r.z + token) - (double)r.zmax) * r.scale * kLn2 - log(total));
   }
 }
 
 // shared memory behind the stages: scales, table, row bits, barriers
-constexpr int kHeadExtra = HEAD_ROWS * 8 + kExpTab * 8 + 32 + 8 * (2 * HL_MAX_STAGES + 5) + 16;
+constexpr int kHeadExtra = HEAD_ROWS * 12 + kExpTab * 8 + HEAD_ROWS / 8 + 8 * (2 * HL_MAX_STAGES + 5) + 16;
 
 int head_logits_stages(int nt) {
   const int fit = (227 * 1024 - 1024 - kHeadExtra) / (A_STAGE_BYTES + nt * 64);
   return fit < HL_MAX_STAGES ? fit : HL_MAX_STAGES;
 }
 
-// tmC: C in boxes of {64, 128}; tmE: E in boxes of {64, nt / 2}; grid: an even number of CTAs.
-cudaError_t launch_head_logits(const CUtensorMap& tmC, const CUtensorMap& tmE, const HeadArgs& a, int grid,
-                               cudaStream_t stream) {
+// tmC, tmC32: C in boxes of {64, 128} and {64, 32}; tmE: E in boxes of {64, nt / 2}; grid: an even number of CTAs.
+cudaError_t launch_head_logits(const CUtensorMap& tmC, const CUtensorMap& tmC32, const CUtensorMap& tmE,
+                               const HeadArgs& a, int grid, cudaStream_t stream) {
   const size_t smem = 1024 + (size_t)a.stages * (A_STAGE_BYTES + a.nt * 64) + kHeadExtra;
   cudaError_t e = cudaFuncSetAttribute(head_logits_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  head_logits_kernel<<<grid, HL_THREADS, smem, stream>>>(tmC, tmE, a);
+  head_logits_kernel<<<grid, HL_THREADS, smem, stream>>>(tmC, tmC32, tmE, a);
   return cudaGetLastError();
 }
 
