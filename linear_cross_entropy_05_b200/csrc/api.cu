@@ -1260,17 +1260,17 @@ cce_status_t run_head(const void* E, const void* C, int64_t N, int64_t D, int64_
   a.status = reinterpret_cast<unsigned long long*>(ws);
   a.wait_limit_ns = g_wait_limit_ns.load();
   a.withhold_loads = g_withhold_loads.load();
-  // The vocabulary is shared out evenly: with tiles dealt whole, 594 tiles on
-  // 74 pairs take as long as 666.
-  const int pairs = sms / 2;
-  a.pair_rows = (a.n_grp + pairs - 1) / pairs * 32;
-  const int grid = 2 * ((a.n_grp * 32 + a.pair_rows - 1) / a.pair_rows);
   int box = 0;
   for (int64_t n0 = 0; n0 < N; n0 += HEAD_ROWS) {
     a.n0 = (int)n0;
     a.n_rows = (int)std::min<int64_t>(N - n0, HEAD_ROWS);
     a.n_blk = (a.n_rows + 255) / 256;
     a.nt = ((a.n_rows + a.n_blk - 1) / a.n_blk + 31) / 32 * 32;  // (a pair's products take multiples of 32 columns)
+    // The vocabulary is shared out evenly: with tiles dealt whole, 594 tiles on
+    // 74 pairs take as long as 666.
+    const int shares = std::max(1, sms / 2 / a.n_blk);
+    a.pair_rows = (a.n_grp + shares - 1) / shares * 32;
+    const int grid = 2 * a.n_blk * ((a.n_grp * 32 + a.pair_rows - 1) / a.pair_rows);
     a.stages = head_logits_stages(a.nt);
     if (a.nt != box && !make_map(&tmE, E, N, D, a.nt / 2)) return CCE_ERR_CUDA;
     box = a.nt;

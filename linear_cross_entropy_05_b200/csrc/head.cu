@@ -130,9 +130,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(HL_THREADS, 1)
   const int lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
-  // this pair's vocabulary entries: whole groups, as many for every pair as
-  // can be; the last tile is loaded as far as it reaches
-  const int va = min(a.V, (blockIdx.x >> 1) * a.pair_rows), vb = min(a.V, va + a.pair_rows);
+  // This pair's block of tokens, and its vocabulary entries: whole groups, as
+  // many for every pair as can be; the last tile is loaded as far as it
+  // reaches.  The pairs of one share of the vocabulary and different blocks
+  // walk it together, so that C is read from memory once (one pair taking the
+  // blocks in turn for each tile found 14 % of the second block's C in L2).
+  const int pair = blockIdx.x >> 1;
+  const int row0 = pair % a.n_blk * a.nt;  // first row of the block
+  const int va = min(a.V, pair / a.n_blk * a.pair_rows), vb = min(a.V, va + a.pair_rows);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
@@ -182,24 +187,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(HL_THREADS, 1)
         const int mine = min(BM / 32, max(0, groups - (int)rank * (BM / 32)));
         const uint32_t bytes = (uint32_t)(groups * 32 * BK * 2 + 2 * a.nt * 64);
         const int y = v0 + (int)rank * BM;
-        // (a second block of tokens finds the tile's rows of C in L2)
-        for (int blk = 0; blk < a.n_blk; ++blk) {
-          for (int kb = 0; kb < nkb; ++kb) {
-            if (!mbar_wait(&empty[stage], phase ^ 1u, wc)) goto producer_done;
-            uint8_t* X = smem + (size_t)stage * stage_bytes;
-            if (leader) mbar_arrive_expect_tx(&full[stage], bytes);
-            if (mine == BM / 32)
-              tma_load_2d_pair(X, &tmC, &full[stage], kb * BK, y);
-            else  // (what the other rows of the stage hold only reaches logits that nobody reads)
-              for (int g = 0; g < mine; ++g)
-                tma_load_2d_pair(X + g * 4096, &tmC32, &full[stage], kb * BK, y + g * 32);
-            tma_load_2d_pair(X + A_STAGE_BYTES, &tmE, &full[stage], kb * BK,
-                             a.n0 + blk * a.nt + (int)rank * (a.nt / 2));
-            armed |= 1u << stage;
-            if (++stage == S) {
-              stage = 0;
-              phase ^= 1u;
-            }
+        for (int kb = 0; kb < nkb; ++kb) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, wc)) goto producer_done;
+          uint8_t* X = smem + (size_t)stage * stage_bytes;
+          if (leader) mbar_arrive_expect_tx(&full[stage], bytes);
+          if (mine == BM / 32)
+            tma_load_2d_pair(X, &tmC, &full[stage], kb * BK, y);
+          else  // (what the other rows of the stage hold only reaches logits that nobody reads)
+            for (int g = 0; g < mine; ++g)
+              tma_load_2d_pair(X + g * 4096, &tmC32, &full[stage], kb * BK, y + g * 32);
+          tma_load_2d_pair(X + A_STAGE_BYTES, &tmE, &full[stage], kb * BK, a.n0 + row0 + (int)rank * (a.nt / 2));
+          armed |= 1u << stage;
+          if (++stage == S) {
+            stage = 0;
+            phase ^= 1u;
           }
         }
       }
@@ -217,7 +218,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(HL_THREADS, 1)
       const uint32_t idesc = idesc_bf16_f32(2 * BM, a.nt, false, false);
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
-      for (int t = 0; t < a.n_blk * ((vb - va + BN - 1) / BN); ++t) {
+      for (int v0 = va; v0 < vb; v0 += BN) {
         if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, wc)) goto mma_done;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(acc * 256);
@@ -259,9 +260,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(HL_THREADS, 1)
     const uint32_t tempty_leader1 = mapa_shared(smem_u32(&tempty[1]), 0);
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int t = 0; t < a.n_blk * ((vb - va + BN - 1) / BN); ++t) {
-      const int v0 = va + t / a.n_blk * BN, row0 = t % a.n_blk * a.nt;  // first row of the block of tokens
-      const int n_chunk = (min(a.nt, a.n_rows - row0) + 31) / 32;
+    const int n_chunk = (min(a.nt, a.n_rows - row0) + 31) / 32;
+    for (int v0 = va; v0 < vb; v0 += BN) {
       const bool ready = __all_sync(0xffffffffu, mbar_wait(&tfull[acc], acc_phase, wc));
       if (!ready) break;
       tc_fence_after();
