@@ -375,8 +375,8 @@ CCE_API cce_status_t cce_distill_backward(const void* E, const void* C, const in
 
 /* Workspace bytes of cce_top_logits and cce_sample (0 if the sizes are
  * invalid): the logits of min(N, 512) tokens in fp32 (524 MB at 512 tokens and
- * 256000 entries), 12 bytes per token and 32 vocabulary entries, and the
- * status block. */
+ * 256000 entries), 12 bytes per token and 32 vocabulary entries, 12 KB
+ * per token, and 12.5 KB. */
 CCE_API size_t cce_head_workspace_size(int64_t N, int64_t D, int64_t V);
 
 /* The k largest logits of every token in falling order (values [N x k] fp32,

@@ -1225,11 +1225,12 @@ bool head_sizes_ok(int64_t N, int64_t D, int64_t V) {
   return sizes_ok(N, D, V) && V <= INT_MAX - 2 * BN;
 }
 
-// Workspace: status | a chunk's logits [rows][ld] fp32 | group sums
-// [rows][n_grp] fp64 | group maxima [rows][n_grp] fp32.
+// Workspace: status | 2^-x table | the rows' scales | a chunk's logits [rows][ld] fp32 | group sums
+// [rows][n_grp] fp64 | group maxima [rows][n_grp] fp32 | the bins' sums and
+// maxima [rows][HEAD_BINS].
 struct HeadLayout {
   int rows, n_grp, ld;
-  size_t off_logits, off_mass, off_max, bytes;
+  size_t off_tab, off_scales, off_logits, off_mass, off_max, off_bmass, off_bmax, bytes;
 };
 
 HeadLayout plan_head(int64_t N, int64_t V) {
@@ -1237,10 +1238,14 @@ HeadLayout plan_head(int64_t N, int64_t V) {
   L.rows = (int)std::min<int64_t>(N, HEAD_ROWS);
   L.n_grp = (int)((V + 31) / 32);
   L.ld = L.n_grp * 32;
-  L.off_logits = STATUS_BYTES;
+  L.off_tab = STATUS_BYTES;
+  L.off_scales = L.off_tab + HEAD_EXP_TAB * 8;
+  L.off_logits = L.off_scales + HEAD_ROWS * 8;
   L.off_mass = L.off_logits + align_up((size_t)L.rows * L.ld * 4, 256);
   L.off_max = L.off_mass + align_up((size_t)L.rows * L.n_grp * 8, 256);
-  L.bytes = L.off_max + align_up((size_t)L.rows * L.n_grp * 4, 256);
+  L.off_bmass = L.off_max + align_up((size_t)L.rows * L.n_grp * 4, 256);
+  L.off_bmax = L.off_bmass + (size_t)L.rows * HEAD_BINS * 8;
+  L.bytes = L.off_bmax + (size_t)L.rows * HEAD_BINS * 4;
   return L;
 }
 
@@ -1254,9 +1259,13 @@ cce_status_t run_head(const void* E, const void* C, int64_t N, int64_t D, int64_
   a.V = (int)V;
   a.n_grp = L.n_grp;
   a.ld = L.ld;
+  a.exp_tab = reinterpret_cast<double*>(ws + L.off_tab);
+  a.scales = reinterpret_cast<double*>(ws + L.off_scales);
   a.logits = reinterpret_cast<float*>(ws + L.off_logits);
   a.gmass = reinterpret_cast<double*>(ws + L.off_mass);
   a.gmax = reinterpret_cast<float*>(ws + L.off_max);
+  a.bmass = reinterpret_cast<double*>(ws + L.off_bmass);
+  a.bmax = reinterpret_cast<float*>(ws + L.off_bmax);
   a.status = reinterpret_cast<unsigned long long*>(ws);
   a.wait_limit_ns = g_wait_limit_ns.load();
   a.withhold_loads = g_withhold_loads.load();
@@ -1268,9 +1277,11 @@ cce_status_t run_head(const void* E, const void* C, int64_t N, int64_t D, int64_
     a.nt = ((a.n_rows + a.n_blk - 1) / a.n_blk + 31) / 32 * 32;  // (a pair's products take multiples of 32 columns)
     // The vocabulary is shared out evenly: with tiles dealt whole, 594 tiles on
     // 74 pairs take as long as 666.
-    const int shares = std::max(1, sms / 2 / a.n_blk);
+    const int shares = std::min(HEAD_BINS / 8, std::max(1, sms / 2 / a.n_blk));
     a.pair_rows = (a.n_grp + shares - 1) / shares * 32;
-    const int grid = 2 * a.n_blk * ((a.n_grp * 32 + a.pair_rows - 1) / a.pair_rows);
+    const int used = (int)(((int64_t)a.n_grp * 32 + a.pair_rows - 1) / a.pair_rows);
+    a.n_bin = 8 * used;
+    const int grid = 2 * a.n_blk * used;
     a.stages = head_logits_stages(a.nt);
     if (a.nt != box && !make_map(&tmE, E, N, D, a.nt / 2)) return CCE_ERR_CUDA;
     box = a.nt;

@@ -127,17 +127,24 @@ struct DistillFinArgs {
 
 // The head's logits of a chunk of tokens and the choice among them (head.cu).
 constexpr int HEAD_ROWS = 512;  // tokens per chunk
+constexpr int HEAD_EXP_TAB = 1024;
+constexpr int HEAD_BINS = 1024; // bins per row: eight for each of at most 128 shares of the vocabulary
 struct HeadArgs {
   int D, V;
   int n0, n_rows;      // the chunk's tokens: n0 .. n0 + n_rows - 1, n_rows <= HEAD_ROWS
   int n_blk, nt;       // blocks of tokens, and tokens of a block (a multiple of 32, at most 256)
   int n_grp;           // groups of 32 vocabulary entries
-  int pair_rows;       // vocabulary entries of each CTA pair (a multiple of 32)
+  int pair_rows;       // vocabulary entries of each CTA pair, a share (a multiple of 32)
+  int n_bin;           // eight for each share
   int stages;
   int ld;              // floats from one token's logits to the next's
   float* logits;       // [n_rows][ld]
   float* gmax;         // [n_rows][n_grp] largest logit of each group
-  double* gmass;       // [n_rows][n_grp] sum exp((z - gmax) / T)
+  double* gmass;       // [n_rows][n_grp] sum exp((z - gmax) / T), where 32 rows hold a draw that needs it
+  double* exp_tab;     // [HEAD_EXP_TAB] 2^-(i / HEAD_EXP_TAB), for head_select
+  double* scales;      // [n_rows] log2(e) / T, for head_select
+  float* bmax;         // [n_rows][n_bin] largest logit of each bin
+  double* bmass;       // [n_rows][n_bin] sum exp((z - bmax) / T)
   unsigned long long* status;
   unsigned long long wait_limit_ns;
   int withhold_loads;

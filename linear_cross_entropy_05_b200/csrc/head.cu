@@ -14,16 +14,18 @@
 //               and not 256.  CTA pairs (cta_group::2): 256 vocabulary rows x
 //               up to 256 tokens in TMEM, double buffered; 128 rows of C and
 //               half of the tokens' rows of E per CTA and stage.  The logits
-//               go to the workspace in fp32, and for each group of 32
-//               vocabulary entries the largest one and sum exp(x - largest).
+//               go to the workspace in fp32, with the largest of each group
+//               of 32 vocabulary entries and, for each of a few hundred bins
+//               of groups (the ones that one epilogue warp meets), the largest
+//               and sum exp(x - largest).
 // head_select   one block per token.  Almost no row needs its logits again:
-//               the groups' largest values bound the k-th largest logit (the
-//               k-th largest group maximum is no larger), so only the groups
-//               that reach the bound are read, and their few candidates are
-//               sorted in shared memory; a draw without filters walks the
-//               groups' sums and reads one group.  Rows that this does not
-//               settle (more than kCap candidates: a wide nucleus, a row full
-//               of ties) take exact passes over the whole row.
+//               the k-th largest bin maximum is no larger than the k-th
+//               largest logit, so only the bins, and of these the groups, that
+//               reach it are read, and their few candidates are sorted in
+//               shared memory; a draw without filters walks the bins' sums,
+//               the groups' of one share, and reads one group.  Rows that
+//               this does not settle (more than kCap candidates: a wide
+//               nucleus, a row full of ties) take exact passes over the row.
 //
 // A drawn token is decided by comparing u with a quotient of sums of up to V
 // exponentials; these sums are formed in double (the groups' in 2^-52 fixed
@@ -42,6 +44,7 @@ namespace {
 
 constexpr int HL_EPI_WARPS = 16;                 // four per TMEM lane group, taking 32-token chunks in turn
 constexpr int HL_THREADS = 64 + 32 * HL_EPI_WARPS;
+constexpr int HL_CHUNKS = 8 / (HL_EPI_WARPS / 4); // 32-token chunks of a warp: of at most eight in 256 tokens
 constexpr int HL_MAX_STAGES = 12;
 constexpr double kLog2e = 1.4426950408889634074;
 
@@ -60,7 +63,7 @@ constexpr unsigned kKeyNegInf = 0x007fffffu;  // order_key(-inf)
 // |r| <= 1 / 2048, 2^-(k / 1024) from a table (and the exponent) and 2^-r from
 // its series up to r^3 (the next term is below 6e-16).  A fraction of the
 // double operations of a general exp2.
-constexpr int kExpTab = 1024;
+constexpr int kExpTab = HEAD_EXP_TAB;
 __device__ __forceinline__ void fill_exp_table(double* tab) {
   for (int i = threadIdx.x; i < kExpTab; i += blockDim.x) tab[i] = exp2(-(double)i / kExpTab);
 }
@@ -116,7 +119,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(HL_THREADS, 1)
   double* tab = reinterpret_cast<double*>(smem + (size_t)S * stage_bytes);
   double* scale = tab + kExpTab;                                          // [HEAD_ROWS] log2(e) / T
   float* scale_f = reinterpret_cast<float*>(scale + HEAD_ROWS);           // [HEAD_ROWS]
-  unsigned* exact = reinterpret_cast<unsigned*>(scale_f + HEAD_ROWS);     // a bit per row: row_exact
+  // running largest logit and sum exp of each epilogue warp's share of the
+  // vocabulary, for its columns [warp][chunk][lane]
+  double* bin_sum = reinterpret_cast<double*>(scale_f + HEAD_ROWS);
+  float* bin_max = reinterpret_cast<float*>(bin_sum + HL_EPI_WARPS * HL_CHUNKS * 32);
+  unsigned* exact = reinterpret_cast<unsigned*>(bin_max + HL_EPI_WARPS * HL_CHUNKS * 32);  // a bit per row: row_exact
   uint64_t* bars = reinterpret_cast<uint64_t*>(exact + HEAD_ROWS / 32);
   uint64_t* full = bars;                    // leader: both CTAs' copies landed
   uint64_t* empty = full + HL_MAX_STAGES;   // each CTA: stage free again
@@ -169,6 +176,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(HL_THREADS, 1)
     if (lane == 0) exact[n >> 5] = bits;
   }
   fill_exp_table(tab);
+  for (int i = threadIdx.x; i < HL_EPI_WARPS * HL_CHUNKS * 32; i += HL_THREADS) {
+    bin_max[i] = -INFINITY;
+    bin_sum[i] = 0.0;
+  }
+  if (blockIdx.x == 0) {  // for head_select
+    for (int i = threadIdx.x; i < kExpTab; i += HL_THREADS) a.exp_tab[i] = exp2(-(double)i / kExpTab);
+    for (int i = threadIdx.x; i < a.n_rows; i += HL_THREADS) a.scales[i] = row_scale(a, a.n0 + i);
+  }
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
@@ -179,6 +194,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(HL_THREADS, 1)
   if (warp == 0) {
     if (lane == 0) {
       // ---------------- TMA producer (both CTAs) ----------------
+      // C passes through L2 once: first to leave, so that what head_select reads
+      // (and its code) stays
+      const uint64_t once = l2_policy_evict_first();
       int stage = 0;
       uint32_t phase = 0, armed = 0;
       for (int v0 = a.withhold_loads ? vb : va; v0 < vb; v0 += BN) {
@@ -192,10 +210,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(HL_THREADS, 1)
           uint8_t* X = smem + (size_t)stage * stage_bytes;
           if (leader) mbar_arrive_expect_tx(&full[stage], bytes);
           if (mine == BM / 32)
-            tma_load_2d_pair(X, &tmC, &full[stage], kb * BK, y);
+            tma_load_2d_pair_hint(X, &tmC, &full[stage], kb * BK, y, once);
           else  // (what the other rows of the stage hold only reaches logits that nobody reads)
             for (int g = 0; g < mine; ++g)
-              tma_load_2d_pair(X + g * 4096, &tmC32, &full[stage], kb * BK, y + g * 32);
+              tma_load_2d_pair_hint(X + g * 4096, &tmC32, &full[stage], kb * BK, y + g * 32, once);
           tma_load_2d_pair(X + A_STAGE_BYTES, &tmE, &full[stage], kb * BK, a.n0 + row0 + (int)rank * (a.nt / 2));
           armed |= 1u << stage;
           if (++stage == S) {
@@ -326,11 +344,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(HL_THREADS, 1)
           }
         }
         if (lane < n_here) {
-          // (the eight groups of a tile fill whole sectors of each token's list)
           const size_t at = (size_t)(row + lane) * a.n_grp + grp;
           a.gmax[at] = my_max;
-          a.gmass[at] = in_double ? ((double)my_hi * 67108864.0 + (double)my_lo) * (1.0 / 2251799813685248.0)
-                                  : (double)my_hi * (1.0 / 67108864.0);
+          // this warp's own sum over the tiles
+          const int i = ((warp - 2) * HL_CHUNKS + c / (HL_EPI_WARPS / 4)) * 32 + lane;
+          const float old = bin_max[i], top = fmaxf(old, my_max);
+          double mass = (double)my_hi * (1.0 / 67108864.0);
+          if (in_double) {
+            mass = ((double)my_hi * 67108864.0 + (double)my_lo) * (1.0 / 2251799813685248.0);
+            a.gmass[at] = mass;
+          }
+          const double f = scale[row + lane];
+          if (my_max > -INFINITY)
+            bin_sum[i] = bin_sum[i] * exp2_neg(((double)top - (double)old) * f, tab) +
+                         mass * exp2_neg(((double)top - (double)my_max) * f, tab);
+          bin_max[i] = top;
         }
       }
       tc_fence_before();
@@ -339,6 +367,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(HL_THREADS, 1)
       if (++acc == 2) {
         acc = 0;
         acc_phase ^= 1u;
+      }
+    }
+    // this warp's bin: its share of the vocabulary, every eighth group of it
+    const int bin = pair / a.n_blk * 8 + (int)rank * 4 + lg;
+    for (int c = hsel; c < n_chunk; c += HL_EPI_WARPS / 4) {
+      const int i = ((warp - 2) * HL_CHUNKS + c / (HL_EPI_WARPS / 4)) * 32 + lane, row = row0 + c * 32 + lane;
+      if (row < a.n_rows) {
+        a.bmax[(size_t)row * a.n_bin + bin] = bin_max[i];
+        a.bmass[(size_t)row * a.n_bin + bin] = bin_sum[i];
       }
     }
   }
@@ -387,28 +424,31 @@ struct SelectShared {
 struct Row {
   const float* z;       // [V]
   const float* gmax;    // [n_grp]
-  const double* gmass;  // [n_grp]
+  const double* gmass;  // [n_grp] (rows of a chunk with exact ones)
   int V, n_grp;
+  int share;            // groups of a share of the vocabulary; bin b holds every eighth of share b / 8
+  unsigned key[2];      // this thread's bins' largest logits (bins threadIdx.x, + HS_THREADS)
+  unsigned top, low;    // the largest key, and the smallest that is not of an empty bin
   float zmax;
   double scale;         // log2(e) / T
   const double* tab;
 };
 
-// f(group, value) for this thread's groups, eight loads at a time.
-template <typename T, typename F>
-__device__ __forceinline__ void each_group(const T* __restrict__ p, int n, F f) {
-  for (int g0 = threadIdx.x; g0 < n; g0 += 8 * HS_THREADS) {
-    T v[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = g0 + j * HS_THREADS < n ? __ldg(p + g0 + j * HS_THREADS) : T(0);
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (g0 + j * HS_THREADS < n) f(g0 + j * HS_THREADS, v[j]);
-  }
-}
-
 __device__ __forceinline__ unsigned grp_key(const Row& r, const SelectShared& s, int g) {
   return g < kGrpCap ? s.gkey[g] : order_key(__ldg(r.gmax + g));
+}
+// The groups' keys to shared memory, for the paths that go through all groups.
+__device__ void load_group_keys(const Row& r, SelectShared& s) {
+  const int n = min(r.n_grp, kGrpCap);
+  for (int g0 = threadIdx.x; g0 < n; g0 += 8 * HS_THREADS) {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = g0 + j * HS_THREADS < n ? __ldg(r.gmax + g0 + j * HS_THREADS) : 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (g0 + j * HS_THREADS < n) s.gkey[g0 + j * HS_THREADS] = order_key(v[j]);
+  }
+  __syncthreads();
 }
 // exp((z - zmax) / T)
 __device__ __forceinline__ double mass_of(const Row& r, float z) {
@@ -505,34 +545,36 @@ __device__ unsigned radix_select(int n, int want, KeyFn key, SelectShared& s, in
   return prefix;
 }
 
-// A key that at least `want` group maxima reach (1 <= want <= n_grp), and not
-// many more.  mine: the largest key of this thread's groups.  For few, the
-// threads' largest keys stand for all groups (the want-th largest of 512 bins'
-// maxima is a bound too, and seldom a lower one) and are halved by counting
-// threads; else three counts a pass over all groups split the keys between one
-// that is reached often enough and one that is not into four.  Either ends when
-// the number is within half of `want` or the keys are exhausted.  (A radix
-// select's first digits put every group into one bin: 8000 additions to one
-// word a digit, and 77 us for one row of 256000 entries.)
-__device__ unsigned group_threshold(const Row& r, int want, unsigned mine, unsigned top, unsigned bottom,
-                                    SelectShared& s) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  unsigned lo = bottom, hi = top + 1u;  // count(>= lo) >= want > count(>= hi)
-  const int enough = want + want / 2 + 16;
-  if (want <= HS_THREADS / 4 && r.n_grp >= HS_THREADS) {
-    lo = block_pick<false>(mine, s);
-    while (hi - lo > 1u) {
-      const unsigned mid = lo + (hi - lo) / 2u;
-      const int c = __syncthreads_count(mine >= mid);
-      if (c >= want) {
-        lo = mid;
-        if (c <= enough) break;
-      } else {
-        hi = mid;
-      }
+// A key that at least `want` bin maxima reach, and not many more: halving by
+// counting threads, until the number is within half of `want` or the keys are
+// exhausted; 0 if fewer than 3 / 2 `want` threads have a bin that holds anything
+// (then the bound would be a poor one).  (A radix select's first digits put
+// every group into one bin: 8000 additions to one word a digit, 77 us for one
+// row of 256000 entries.)
+__device__ unsigned bin_threshold(const Row& r, int want, SelectShared& s) {
+  const unsigned mine = max(r.key[0], r.key[1]);
+  unsigned lo = r.low, hi = r.top + 1u;  // count(lo) >= want > count(hi)
+  if (2 * __syncthreads_count(mine >= lo) < 3 * want) return 0u;
+  while (hi - lo > 1u) {
+    const unsigned mid = lo + (hi - lo) / 2u;
+    const int c = __syncthreads_count(mine >= mid);
+    if (c >= want) {
+      lo = mid;
+      if (c <= want + want / 2 + 16) break;
+    } else {
+      hi = mid;
     }
-    return lo;
   }
+  return lo;
+}
+
+// The same over all groups (1 <= want <= n_grp), with three counts a pass that
+// split the keys between one that is reached often enough and one that is not
+// into four.
+__device__ unsigned group_threshold(const Row& r, int want, SelectShared& s) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  unsigned lo = 0u, hi = r.top + 1u;
+  const int enough = want + want / 2 + 16;
   while (hi - lo > 1u) {
     const unsigned step = max(1u, (hi - lo) / 4u);
     const unsigned t1 = lo + step, t2 = min(hi, t1 + step), t3 = min(hi, t2 + step);
@@ -579,66 +621,130 @@ __device__ unsigned group_threshold(const Row& r, int want, unsigned mine, unsig
 }
 
 // Appends every entry with key >= thr to s.cand (as far as it fits); their
-// number, or one above kCap, is returned to all threads.
-__device__ int gather_candidates(const Row& r, unsigned thr, SelectShared& s) {
+// number, or one above kCap, is returned to all threads.  by_bins: the groups
+// to read are looked up among the bins that reach thr, else among all (whose
+// keys have been loaded).
+__device__ int gather_candidates(const Row& r, unsigned thr, bool by_bins, SelectShared& s) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  constexpr int kBins = 2 * HS_THREADS;
+  int* groups = s.list + kBins;  // room for 2 kCap - kBins
   __syncthreads();
   if (threadIdx.x == 0) {
     s.count = 0;
     s.found_rank = 0;
+    s.out_i = 0;
   }
   __syncthreads();
-#pragma unroll 4
-  for (int g = threadIdx.x; g < r.n_grp; g += HS_THREADS)
-    if (grp_key(r, s, g) >= thr) {
-      const int at = atomicAdd(&s.found_rank, 1);
-      if (at < 2 * kCap) s.list[at] = g;
+  // one addition per warp for the lanes that have a group
+  auto add_groups = [&](bool has, int g) {
+    const unsigned who = __ballot_sync(0xffffffffu, has);
+    if (who == 0u) return;
+    int at = 0;
+    if (lane == 0) at = atomicAdd(&s.found_rank, __popc(who));
+    at = __shfl_sync(0xffffffffu, at, 0) + __popc(who & ((1u << lane) - 1u));
+    if (has && at < 2 * kCap - kBins) groups[at] = g;
+  };
+  if (by_bins) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const bool has = r.key[i] >= thr;
+      const unsigned who = __ballot_sync(0xffffffffu, has);
+      int at = 0;
+      if (lane == 0 && who) at = atomicAdd(&s.out_i, __popc(who));
+      at = __shfl_sync(0xffffffffu, at, 0) + __popc(who & ((1u << lane) - 1u));
+      if (has) s.list[at] = threadIdx.x + i * HS_THREADS;
     }
+    __syncthreads();
+    // a lane per group of a bin, four bins a turn
+    const int n_bins = s.out_i;
+    for (int i = w; i < n_bins; i += 4 * HS_WARPS) {
+      for (int t = 0; t * 8 < r.share; t += 32) {
+        unsigned key[4];
+        int g[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int bin = i + q * HS_WARPS < n_bins ? s.list[i + q * HS_WARPS] : 0;
+          const int in_share = (t + lane) * 8 + (bin & 7);
+          g[q] = (bin >> 3) * r.share + in_share;
+          const bool there = i + q * HS_WARPS < n_bins && in_share < r.share && g[q] < r.n_grp;
+          key[q] = there ? order_key(__ldg(r.gmax + g[q])) : 0u;
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) add_groups(key[q] >= thr, g[q]);
+      }
+    }
+  } else {
+    for (int g0 = 0; g0 < r.n_grp; g0 += HS_THREADS) {
+      const int g = g0 + (int)threadIdx.x;
+      add_groups(g < r.n_grp && grp_key(r, s, g) >= thr, g);
+    }
+  }
   __syncthreads();
   const int n_list = s.found_rank;
   if (n_list > kCap) return kCap + 1;  // a candidate at least from each
-  for (int i = w; i < n_list; i += 4 * HS_WARPS) {
-    // four groups a turn, so that their loads overlap
-    float z[4];
-    int v[4];
+  for (int i = w; i < n_list; i += 8 * HS_WARPS) {
+    // eight groups a turn, so that their loads overlap
+    float z[8];
+    int v[8], total = 0;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < 8; ++q) {
       const int at = i + q * HS_WARPS;
-      v[q] = at < n_list ? s.list[at] * 32 + lane : r.V;
+      v[q] = at < n_list ? groups[at] * 32 + lane : r.V;
       z[q] = v[q] < r.V ? __ldg(r.z + v[q]) : 0.f;
     }
+    unsigned hits[8];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const unsigned k = order_key(z[q]);
-      const bool hit = v[q] < r.V && k >= thr;
-      const unsigned hits = __ballot_sync(0xffffffffu, hit);
-      int base = 0;
-      if (lane == 0 && hits) base = atomicAdd(&s.count, __popc(hits));
-      base = __shfl_sync(0xffffffffu, base, 0);
-      const int at = base + __popc(hits & ((1u << lane) - 1u));
-      if (hit && at < kCap) s.cand[at] = ((unsigned long long)(~k) << 32) | (unsigned)v[q];
+    for (int q = 0; q < 8; ++q) {
+      hits[q] = __ballot_sync(0xffffffffu, v[q] < r.V && order_key(z[q]) >= thr);
+      total += __popc(hits[q]);
+    }
+    int at = 0;
+    if (lane == 0) at = atomicAdd(&s.count, total);
+    at = __shfl_sync(0xffffffffu, at, 0);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int mine = at + __popc(hits[q] & ((1u << lane) - 1u));
+      if ((hits[q] >> lane & 1u) && mine < kCap)
+        s.cand[mine] = ((unsigned long long)(~order_key(z[q])) << 32) | (unsigned)v[q];
+      at += __popc(hits[q]);
     }
   }
   __syncthreads();
   return s.count;
 }
 
-// How many of n <= HS_THREADS entries are below this thread's (threads 0 .. n - 1
-// hold one each): below(j) tells whether entry j is.  The comparisons of an
-// entry are shared by HS_THREADS / n threads.
+// Candidates: every entry not below some key that at least `want` groups reach
+// (their number as of gather_candidates); thr: that key, or `floor` if that is
+// larger.
+__device__ int gather_top_groups(const Row& r, int want, unsigned floor, unsigned& thr, SelectShared& s) {
+  thr = bin_threshold(r, want, s);
+  if (thr) {
+    thr = max(floor, thr);
+    return gather_candidates(r, thr, true, s);
+  }
+  load_group_keys(r, s);
+  thr = max(floor, want < r.n_grp ? group_threshold(r, want, s) : 0u);
+  return gather_candidates(r, thr, false, s);
+}
+
+// How many of n <= HS_THREADS values value(0 .. n - 1) are below this thread's,
+// value(threadIdx.x).  The comparisons of a value are shared by HS_THREADS / n
+// threads.
 template <typename Fn>
-__device__ int block_rank(int n, Fn below, SelectShared& s) {
+__device__ int block_rank(int n, Fn value, SelectShared& s) {
   int m = 32;
   while (m < n) m <<= 1;
   const int i = threadIdx.x & (m - 1), parts = HS_THREADS / m, part = threadIdx.x / m;
   __syncthreads();
   s.rank[threadIdx.x] = 0;
   __syncthreads();
-  int c = 0;
-  if (i < n)
-#pragma unroll 4
-    for (int j = part; j < n; j += parts) c += below(i, j);
-  if (c) atomicAdd(&s.rank[i], c);
+  if (i < n) {
+    const auto mine = value(i);
+    int c = 0;
+#pragma unroll 8
+    for (int j = part; j < n; j += parts) c += value(j) < mine;
+    if (c) atomicAdd(&s.rank[i], c);
+  }
   __syncthreads();
   return s.rank[threadIdx.x];
 }
@@ -646,7 +752,7 @@ __device__ int block_rank(int n, Fn below, SelectShared& s) {
 // Sorts s.cand[0 .. n) ascending (n <= kCap; the rest up to a power of two is filled).
 __device__ void sort_candidates(SelectShared& s, int n) {
   if (n <= HS_THREADS) {
-    const int rank = block_rank(n, [&](int i, int j) { return (int)(s.cand[j] < s.cand[i]); }, s);
+    const int rank = block_rank(n, [&](int i) { return s.cand[i]; }, s);
     const unsigned long long mine = (int)threadIdx.x < n ? s.cand[threadIdx.x] : 0ull;
     __syncthreads();
     if ((int)threadIdx.x < n) s.cand[rank] = mine;
@@ -716,14 +822,12 @@ __device__ int gather_exact(const Row& r, unsigned kappa, int ties, SelectShared
 
 // The k largest entries (k <= kCap, k <= V) as candidates: at least these,
 // sorted; their number.
-__device__ int top_candidates(const Row& r, int k, unsigned mine, unsigned top, unsigned bottom, SelectShared& s) {
+__device__ int top_candidates(const Row& r, int k, SelectShared& s) {
   int c = kCap + 1, rank;
-  if (r.n_grp >= k)
-    c = gather_candidates(r, group_threshold(r, k, mine, top, bottom, s), s);
-  else if (r.V <= kCap)
-    c = gather_candidates(r, 0u, s);
+  unsigned thr;
+  if (r.n_grp >= k || r.V <= kCap) c = gather_top_groups(r, k, 0u, thr, s);
   if (c > kCap) {
-    const unsigned thr = radix_select(r.V, k, [&](int v) { return order_key(__ldg(r.z + v)); }, s, rank);
+    thr = radix_select(r.V, k, [&](int v) { return order_key(__ldg(r.z + v)); }, s, rank);
     c = gather_exact(r, thr, rank, s);
   }
   sort_candidates(s, c);
@@ -839,75 +943,63 @@ __device__ int wide_draw(const Row& r, int k, double p, double min_p, double u, 
 }
 
 // Draw without filters: the first id whose cumulated mass passes u times the
-// whole, from the groups' sums and one group's logits.  Each warp has a
-// contiguous share of the groups.
-__device__ int plain_draw(const Row& r, double u, SelectShared& s, double& total) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const int per = ((r.n_grp + HS_WARPS - 1) / HS_WARPS + 31) / 32 * 32;
-  const int ga = min(r.n_grp, w * per), gb = min(r.n_grp, ga + per);
-  auto weight = [&](int g) {
-    return g < gb ? __ldg(r.gmass + g) * mass_of(r, key_value(grp_key(r, s, g))) : 0.0;
-  };
-  double m = 0.0;
-#pragma unroll 8
-  for (int g = ga + lane; g < gb; g += 32) m += weight(g);
+// whole, from the bins' sums (mass[]: this thread's bins'), the groups' sums of
+// one share and one group's logits.
+__device__ int plain_draw(const Row& r, const double (&mass)[2], double u, double& total, SelectShared& s) {
+  const int lane = threadIdx.x & 31;
+  // a share's sum: that of its eight bins
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
-  __syncthreads();
-  if (lane == 0) s.red[w] = m;
-  __syncthreads();
-  double before = 0.0;
-  int owner = 0;
-  total = 0.0;
-  for (int i = 0; i < HS_WARPS; ++i) total += s.red[i];
-  const double target = u * total;
-  // the warp whose share holds the target: the last that begins at or below it
-  double run = 0.0;
-  for (int i = 0; i < HS_WARPS; ++i) {
-    if (s.red[i] > 0.0 && run <= target) {
-      owner = i;
-      before = run;
-    }
-    run += s.red[i];
-  }
-  if (w == owner) {
-    double left = target - before;  // of the mass from group ga on
-    int best = ga;
-    double best_left = left;
-    for (int g0 = ga; g0 < gb; g0 += 32) {
-      const double own = weight(g0 + lane);
-      double inc = own;
+  for (int i = 0; i < 2; ++i) {
+    double m = mass[i];
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double x = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += x;
-      }
-      const unsigned any = __ballot_sync(0xffffffffu, own > 0.0);
-      const unsigned over = __ballot_sync(0xffffffffu, own > 0.0 && inc > left);
-      if (any) {
-        // the first group that passes the target, else the last one so far
-        const int l = over ? __ffs((int)over) - 1 : 31 - __clz((int)any);
-        best = g0 + l;
-        best_left = left - __shfl_sync(0xffffffffu, inc - own, l);
-      }
-      if (over) break;
-      left -= __shfl_sync(0xffffffffu, inc, 31);
-    }
-    const int v = best * 32 + lane;
-    const double own = v < r.V ? mass_of(r, __ldg(r.z + v)) : 0.0;
-    double inc = own;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double x = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += x;
-    }
-    const unsigned any = __ballot_sync(0xffffffffu, own > 0.0);
-    const unsigned over = __ballot_sync(0xffffffffu, own > 0.0 && inc > best_left);
-    const int l = over ? __ffs((int)over) - 1 : 31 - __clz((int)any);
-    if (lane == 0) s.out_i = best * 32 + l;
+    for (int o = 4; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+    if ((lane & 7) == 0) s.mass[(threadIdx.x + i * HS_THREADS) / 8] = m;
   }
   __syncthreads();
-  return s.out_i;
+  constexpr int kShares = HEAD_BINS / 8;
+  double m = threadIdx.x < kShares ? s.mass[threadIdx.x] : 0.0;
+  double before = block_scan(m, s, total);
+  double left = u * total;
+  // the share that holds the target: the last that begins at or below it
+  unsigned at = block_pick<true>(m > 0.0 && before <= left ? threadIdx.x + 1u : 0u, s);
+  const int share = at ? (int)at - 1 : 0;
+  if ((int)threadIdx.x == share) s.red[0] = before;
+  __syncthreads();
+  left -= s.red[0];
+  __syncthreads();
+  // its groups, and the first of them that passes the target (else the last with any mass)
+  const int ga = share * r.share, gb = min(r.n_grp, ga + r.share);
+  int best = ga;
+  double best_left = left;
+  for (int g0 = ga; g0 < gb; g0 += HS_THREADS) {
+    const int g = g0 + (int)threadIdx.x;
+    m = g < gb ? __ldg(r.gmass + g) * mass_of(r, __ldg(r.gmax + g)) : 0.0;
+    double here;
+    before = block_scan(m, s, here);
+    const unsigned over = block_pick<false>(m > 0.0 && before + m > left ? threadIdx.x : 0x7fffffffu, s);
+    at = over != 0x7fffffffu ? over + 1u : block_pick<true>(m > 0.0 ? threadIdx.x + 1u : 0u, s);
+    if (at) {
+      best = g0 + (int)at - 1;
+      if (threadIdx.x + 1u == at) s.red[0] = before;
+      __syncthreads();
+      best_left = left - s.red[0];
+      __syncthreads();
+    }
+    if (over != 0x7fffffffu) break;
+    left -= here;
+  }
+  // its entries (every warp alike)
+  const int v = best * 32 + lane;
+  const double own = v < r.V ? mass_of(r, __ldg(r.z + v)) : 0.0;
+  double inc = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double x = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += x;
+  }
+  const unsigned any = __ballot_sync(0xffffffffu, own > 0.0);
+  const unsigned over = __ballot_sync(0xffffffffu, own > 0.0 && inc > best_left);
+  return best * 32 + (over ? __ffs((int)over) - 1 : 31 - __clz((int)any));
 }
 
 // Draw from sorted candidates that hold every kept entry; k = 0: no top-k.
@@ -924,7 +1016,7 @@ __device__ int draw_from_candidates(const Row& r, int c, int k, double p, double
     // (both filters leave a prefix)
     const int n = __syncthreads_count(i < c && (i == 0 || p >= 1.0 || before < p * total) && e >= min_p);
     if (n <= 1) return (int)(unsigned)s.cand[0];
-    const int rank = block_rank(n, [&](int x, int y) { return (int)((unsigned)s.cand[y] < (unsigned)s.cand[x]); }, s);
+    const int rank = block_rank(n, [&](int x) { return (unsigned)s.cand[x]; }, s);
     if (i < n) {
       s.cand[rank] = mine & 0xffffffffull;
       s.mass[rank] = e;
@@ -984,24 +1076,32 @@ __device__ int draw_from_candidates(const Row& r, int c, int k, double p, double
   return (int)(s.cand[pick] >> 32);
 }
 
-__device__ int sample_row(const Row& r, int k, double p, double min_p, double u, double& total, bool greedy,
-                          unsigned mine, unsigned top_key, unsigned bottom_key, SelectShared& s) {
+__device__ int sample_row(const Row& r, const double (&mass)[2], int k, double p, double min_p, double u,
+                          double& total, bool greedy, SelectShared& s) {
   if (k >= r.V || k < 0) k = 0;
   if (greedy || k == 1) {
     // the lowest id among the largest logits
-    unsigned g_first = 0xffffffffu;
-    for (int g = threadIdx.x; g < r.n_grp; g += HS_THREADS)
-      if (grp_key(r, s, g) == top_key) {
-        g_first = (unsigned)g;
-        break;
+    unsigned g_first = 0x7fffffffu;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (r.key[i] == r.top) {
+        const int bin = threadIdx.x + i * HS_THREADS, g0 = (bin >> 3) * r.share;
+        for (int j = bin & 7; j < r.share && g0 + j < r.n_grp; j += 8)
+          if (order_key(__ldg(r.gmax + g0 + j)) == r.top) {
+            g_first = min(g_first, (unsigned)(g0 + j));
+            break;
+          }
       }
-    const int g = (int)block_pick<false>(g_first, s);
+    const int g = min((int)block_pick<false>(g_first, s), r.n_grp - 1);
     const int v = g * 32 + (int)(threadIdx.x & 31);
-    const unsigned eq = __ballot_sync(0xffffffffu, v < r.V && order_key(__ldg(r.z + v)) == top_key);
+    const unsigned eq = __ballot_sync(0xffffffffu, v < r.V && order_key(__ldg(r.z + v)) == r.top);
     return g * 32 + __ffs((int)eq) - 1;
   }
-  if (k == 0 && p >= 1.0 && !(min_p > 0.0)) return plain_draw(r, u, s, total);
-  if (k > 0 && k <= kCap) return draw_from_candidates(r, top_candidates(r, k, mine, top_key, bottom_key, s), k, p, min_p, u, total, s);
+  if (k == 0 && p >= 1.0 && !(min_p > 0.0)) return plain_draw(r, mass, u, total, s);
+  if (k > 0 && k <= kCap) {
+    const int c = top_candidates(r, k, s);
+    return draw_from_candidates(r, c, k, p, min_p, u, total, s);
+  }
   if (k == 0) {
     // entries below min_p of the largest are out (a little slack: their own
     // masses decide); of the others, groups in growing numbers until their
@@ -1009,13 +1109,15 @@ __device__ int sample_row(const Row& r, int k, double p, double min_p, double u,
     unsigned floor_key = 0u;
     if (min_p > 0.0) {
       const double t = (double)r.zmax + log2(min_p) / r.scale;
-      floor_key = min(top_key, order_key((float)(t - 1e-6 * (fabs(t) + fabs((double)r.zmax) + 1.0))));
+      floor_key = min(r.top, order_key((float)(t - 1e-6 * (fabs(t) + fabs((double)r.zmax) + 1.0))));
     }
     for (int want = 64; want <= 4096; want <<= 3) {
-      unsigned thr = 0u;
-      if (want < r.n_grp && p < 1.0) thr = group_threshold(r, want, mine, top_key, bottom_key, s);
-      thr = max(thr, floor_key);
-      const int c = gather_candidates(r, thr, s);
+      unsigned thr = floor_key;
+      int c;
+      if (p < 1.0)
+        c = gather_top_groups(r, want, floor_key, thr, s);
+      else
+        c = gather_candidates(r, thr, true, s);
       if (c > kCap) break;
       double m = 0.0;
       for (int i = threadIdx.x; i < c; i += HS_THREADS) m += mass_of(r, key_value(cand_key(s.cand[i])));
@@ -1031,7 +1133,7 @@ __device__ int sample_row(const Row& r, int k, double p, double min_p, double u,
 
 }  // namespace
 
-__global__ void __launch_bounds__(HS_THREADS, 1) head_select_kernel(const HeadArgs a) {
+__global__ void __launch_bounds__(HS_THREADS, 2) head_select_kernel(const HeadArgs a) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   SelectShared& s = *reinterpret_cast<SelectShared*>(smem_raw);
   const int n = blockIdx.x;          // row of this chunk
@@ -1043,22 +1145,24 @@ __global__ void __launch_bounds__(HS_THREADS, 1) head_select_kernel(const HeadAr
   r.gmass = a.gmass + (size_t)n * a.n_grp;
   r.V = a.V;
   r.n_grp = a.n_grp;
-  r.scale = row_scale(a, row);
-
+  r.scale = __ldg(a.scales + n);
   r.tab = s.tab;
-  fill_exp_table(s.tab);
-  unsigned mine = 0u, bottom = 0xffffffffu;
-  each_group(r.gmax, r.n_grp, [&](int g, float v) {
-    const unsigned k = order_key(v);
-    if (g < kGrpCap) s.gkey[g] = k;
-    mine = max(mine, k);
-    bottom = min(bottom, k);
-  });
-  const unsigned top = block_pick<true>(mine, s);
-  bottom = block_pick<false>(bottom, s);
-  r.zmax = key_value(top);
+  for (int i = threadIdx.x; i < kExpTab; i += HS_THREADS) s.tab[i] = __ldg(a.exp_tab + i);
+  r.share = a.pair_rows / 32;
+  float bmax[2];
+  double mass[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int bin = threadIdx.x + i * HS_THREADS;
+    bmax[i] = bin < a.n_bin ? __ldg(a.bmax + (size_t)n * a.n_bin + bin) : -INFINITY;
+    mass[i] = bin < a.n_bin ? __ldg(a.bmass + (size_t)n * a.n_bin + bin) : 0.0;
+    r.key[i] = order_key(bmax[i]);
+  }
+  r.top = block_pick<true>(max(r.key[0], r.key[1]), s);
+  r.zmax = key_value(r.top);
+  r.low = block_pick<false>(max(max(r.key[0], r.key[1]), kKeyNegInf + 1u), s);
   const bool timeout = (a.status[ST_FLAGS] & SF_TIMEOUT) != 0;
-  const bool broken = top >= kKeyPosInf || top <= kKeyNegInf;  // an infinite (or NaN) logit on top
+  const bool broken = r.top >= kKeyPosInf || r.top <= kKeyNegInf;  // an infinite (or NaN) logit on top
   if (timeout || broken) {
     if (threadIdx.x == 0 && !timeout) atomicOr(a.status + ST_FLAGS, SF_NONFINITE);
     if (a.u) {
@@ -1075,29 +1179,14 @@ __global__ void __launch_bounds__(HS_THREADS, 1) head_select_kernel(const HeadAr
     }
     return;
   }
-  // sum exp((z - zmax) / T): in double where the token hangs on it (a draw
-  // without filters forms it on its way)
-  const bool exact = row_exact(a, row);
-  const bool plain = exact && !((a.top_p ? a.top_p[row] : a.top_p_all) < 1.f);
-  double total = 0.0;
-  if (!plain) {
-    double m = 0.0;
-    if (exact) {
-      each_group(r.gmass, r.n_grp, [&](int g, double v) { m += v * mass_of(r, key_value(grp_key(r, s, g))); });
-    } else {
-      const float scale = (float)r.scale;
-      float mf = 0.f;
-      each_group(r.gmass, r.n_grp, [&](int g, double v) {
-        mf += (float)v * ex2_approx((key_value(grp_key(r, s, g)) - r.zmax) * scale);
-      });
-      m = (double)mf;
-    }
-    total = block_sum(m, s);
-  }
+  // sum exp((z - zmax) / T) (a draw without filters adds its shares up itself)
+#pragma unroll
+  for (int i = 0; i < 2; ++i) mass[i] *= mass_of(r, bmax[i]);
+  double total = block_sum(mass[0] + mass[1], s);
   constexpr double kLn2 = 0.69314718055994530942;
 
   if (!a.u) {
-    const int c = top_candidates(r, a.k, mine, top, bottom, s);
+    const int c = top_candidates(r, a.k, s);
     for (int i = threadIdx.x; i < a.k; i += HS_THREADS) {
       const unsigned long long cc = i < c ? s.cand[i] : 0ull;
       a.values[(size_t)row * a.k + i] = key_value(cand_key(cc));
@@ -1114,7 +1203,7 @@ __global__ void __launch_bounds__(HS_THREADS, 1) head_select_kernel(const HeadAr
   double min_p = (double)(a.min_p ? a.min_p[row] : a.min_p_all);
   min_p = min_p > 0.0 ? fmin(min_p, 1.0) : 0.0;
   const double u = fmax((double)a.u[row], 0.0);
-  int token = sample_row(r, k, p, min_p, u, total, !(t > 0.f), mine, top, bottom, s);
+  int token = sample_row(r, mass, k, p, min_p, u, total, !(t > 0.f), s);
   if (threadIdx.x == 0) {
     token = min(max(token, 0), a.V - 1);  // (an index into the row whatever the workspace holds)
     a.token[row] = token;
@@ -1123,7 +1212,7 @@ __global__ void __launch_bounds__(HS_THREADS, 1) head_select_kernel(const HeadAr
 }
 
 // shared memory behind the stages: scales, table, row bits, barriers
-constexpr int kHeadExtra = HEAD_ROWS * 12 + kExpTab * 8 + HEAD_ROWS / 8 + 8 * (2 * HL_MAX_STAGES + 5) + 16;
+constexpr int kHeadExtra = HL_EPI_WARPS * HL_CHUNKS * 32 * 12 + HEAD_ROWS * 12 + kExpTab * 8 + HEAD_ROWS / 8 + 8 * (2 * HL_MAX_STAGES + 5) + 16;
 
 int head_logits_stages(int nt) {
   const int fit = (227 * 1024 - 1024 - kHeadExtra) / (A_STAGE_BYTES + nt * 64);

@@ -40,7 +40,7 @@ def test_workspace(L):
     up = lambda x: (x + 255) // 256 * 256  # noqa: E731
     for N, V in ((1, 1), (5, 4096), (256, 256000), (513, 100003), (100000, 33)):
         rows, grp = min(N, 512), -(-V // 32)
-        want = 256 + up(4 * rows * 32 * grp) + up(8 * rows * grp) + up(4 * rows * grp)
+        want = 256 + 8 * (1024 + 512) + up(4 * rows * 32 * grp) + up(8 * rows * grp) + up(4 * rows * grp) + 12 * 1024 * rows
         assert L.cce_head_workspace_size(N, 64, V) == want
     for bad in ((0, 64, 100), (5, 60, 100), (5, 64, 0), (5, 8, (1 << 31) - 1)):
         assert L.cce_head_workspace_size(*bad) == 0

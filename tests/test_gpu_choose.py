@@ -16,15 +16,14 @@ pytestmark = pytest.mark.gpu
 U32 = 2.0 ** -24
 
 # Rows whose token does not hang on it get their log-sum-exp from float
-# exponentials 2^t, t <= 0, of which the error of log S, S = sum 2^t, is at most
+# exponentials 2^t, t <= 0, within each group (summed in double from there), of
+# which the error of log S, S = sum 2^t, is at most
 #   2^-22      ex2's own relative error
 #   30 U32     t is a difference times a factor, each rounded: 2 U32 |t| ln 2
 #              of 2^t, and sum |t| ln 2 2^t / S <= ln V + 1 < 15
 #   2^-22      the 32 terms of a group are rounded to 2^-26 of its largest
 #              (which S holds): 32 * 2^-27
-#   60 U32     a group's sum times its own 2^t (the first two again: 34 U32)
-#              and the float sums over a thread's groups (under 26)
-FLOAT_SUMS = 2.0 ** -21 + 90 * U32
+FLOAT_SUMS = 2.0 ** -21 + 30 * U32
 
 
 def make(seed, N, D, V, spread=2.0, coarse=False):
