@@ -347,13 +347,19 @@ CCE_API size_t cce_distill_forward_workspace_size(int64_t N, int64_t D, int64_t 
 CCE_API size_t cce_distill_backward_workspace_size(int64_t N, int64_t D, int64_t V, int64_t K, unsigned flags);
 
 /* Forward: loss [N] fp32 and lse [N] fp32 (of the logits divided by T; also
- * for rows without a target).  Both are NaN if a bounded wait gave up. */
+ * for rows without a target).  Both are NaN if a bounded wait gave up.
+ * mean, inv_count: fp32 scalars on the device, both or neither null: the mean
+ * of loss over the rows that have an entry (NaN if there is none), and one over
+ * their number. */
 CCE_API cce_status_t cce_distill_forward(const void* E, const void* C, const int64_t* ids, const void* teacher,
                                          int teacher_dtype, int64_t N, int64_t D, int64_t V, int64_t K,
                                          int64_t ignore_index, float temperature, float* loss, float* lse,
-                                         void* workspace, size_t workspace_bytes, void* stream);
+                                         float* mean, float* inv_count, void* workspace, size_t workspace_bytes,
+                                         void* stream);
 
-/* Backward: gradients of sum_i dloss[i] * loss[i],
+/* Backward: gradients of sum_i dloss[i] * loss[i] (dloss_stride 1: dloss [N];
+ * 0: the one value dloss[0] for all rows; times dloss_scale[0] if that is not
+ * null: with inv_count there, the gradient of dloss[0] times the mean),
  *     G[i,v] = dloss[i] T (exp(z_iv / T - lse[i]) - sum_{k: ids[i,k] = v} p[i,k]),
  *     dE = G C,  dC = G^T E,
  * through stripes of G as with CCE_BWD_STRIPES (no entry is filtered).  lse is
@@ -361,8 +367,9 @@ CCE_API cce_status_t cce_distill_forward(const void* E, const void* C, const int
  * CCE_BWD_DETERMINISTIC (dE summed in stripe order), CCE_BWD_BF16_GRADS,
  * CCE_BWD_ACCUMULATE, with their meaning in cce_backward_ex. */
 CCE_API cce_status_t cce_distill_backward(const void* E, const void* C, const int64_t* ids, const void* teacher,
-                                          int teacher_dtype, const float* lse, const float* dloss, int64_t N,
-                                          int64_t D, int64_t V, int64_t K, int64_t ignore_index, float temperature,
+                                          int teacher_dtype, const float* lse, const float* dloss,
+                                          int dloss_stride, const float* dloss_scale, int64_t N, int64_t D,
+                                          int64_t V, int64_t K, int64_t ignore_index, float temperature,
                                           unsigned flags, void* dE, void* dC, void* workspace,
                                           size_t workspace_bytes, void* stream);
 

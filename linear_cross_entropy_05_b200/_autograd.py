@@ -44,19 +44,17 @@ class LinearDistillation(torch.autograd.Function):
     @staticmethod
     def forward(ctx, E, C, ids, teacher, temperature: float, ignore_index: int):
         E, C, ids, teacher = E.contiguous(), C.contiguous(), ids.contiguous(), teacher.contiguous()
-        loss, lse = _distill_forward(E, C, ids, teacher, temperature, ignore_index)
-        keep = ((ids != ignore_index) & (teacher != float("-inf"))).any(1)
-        n = keep.sum()
-        ctx.save_for_backward(E, C, ids, teacher, lse, n)
+        mean, inv_count = (torch.empty((), dtype=torch.float32, device=E.device) for _ in range(2))
+        _, lse = _distill_forward(E, C, ids, teacher, temperature, ignore_index, mean=(mean, inv_count))
+        ctx.save_for_backward(E, C, ids, teacher, lse, inv_count)
         ctx.temperature = temperature
         ctx.ignore_index = ignore_index
-        return loss.sum() / n
+        return mean
 
     @staticmethod
     def backward(ctx, g):
-        E, C, ids, teacher, lse, n = ctx.saved_tensors
-        # rows without an entry have no gradient whatever their dloss
-        dloss = (g.to(torch.float32) / n).expand(E.shape[0]).contiguous()
-        dE, dC = _distill_backward(E, C, ids, teacher, lse, dloss, ctx.temperature, ctx.ignore_index, bf16_grads=True)
+        E, C, ids, teacher, lse, inv_count = ctx.saved_tensors
+        dE, dC = _distill_backward(E, C, ids, teacher, lse, g.to(torch.float32), ctx.temperature, ctx.ignore_index,
+                                   bf16_grads=True, dloss_scale=inv_count)
         need = ctx.needs_input_grad
         return dE if need[0] else None, dC if need[1] else None, None, None, None, None

@@ -5,7 +5,6 @@ library's kernels (cce_distill_forward, cce_distill_backward).
 """
 from __future__ import annotations
 
-import contextlib
 from typing import Optional
 
 import torch
@@ -41,21 +40,26 @@ class Launch:
     current, and what the call allocates is kept from reuse until `stream`
     has passed it when that is not the allocating stream."""
 
+    __slots__ = ("device", "workspace", "stream", "foreign", "guard")
+
     def __init__(self, device, stream, workspace: Optional[Workspace]):
         self.device = device
         self.workspace = workspace or Workspace(device)
-        self.given = stream
-        self.guard = contextlib.ExitStack()
+        self.stream = stream
+        self.guard = None
 
     def __enter__(self):
-        self.guard.enter_context(torch.cuda.device(self.device))
+        if self.device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(self.device)
+            self.guard.__enter__()
         current = torch.cuda.current_stream(self.device)
-        self.stream = current if self.given is None else self.given
+        if self.stream is None:
+            self.stream = current
         self.foreign = self.stream != current
         return self
 
     def __exit__(self, *exc):
-        return self.guard.__exit__(*exc)
+        return self.guard.__exit__(*exc) if self.guard is not None else None
 
     @property
     def ptr(self) -> int:
@@ -89,7 +93,7 @@ def _check_targets(ids, teacher, N, device):
 
 
 def distill_forward(E, C, ids, teacher, temperature: float = 1.0, ignore_index: int = IGNORE_INDEX,
-                    workspace: Optional[Workspace] = None, stream=None, out=None):
+                    workspace: Optional[Workspace] = None, stream=None, out=None, mean=None):
     """Per-token distillation loss and log-sum-exp (fp32 [N]).
 
     ids [N, K] int64 and teacher [N, K] (float32 or bfloat16) hold a teacher's
@@ -98,7 +102,9 @@ def distill_forward(E, C, ids, teacher, temperature: float = 1.0, ignore_index: 
     With p the softmax of a row's teacher logits over its entries at
     `temperature` T and q the student's softmax of E C^T / T over all of the
     vocabulary, loss = T^2 sum_k p_k log(p_k / q_{ids_k}).  lse is the
-    log-sum-exp of the logits divided by T, which distill_backward needs."""
+    log-sum-exp of the logits divided by T, which distill_backward needs.
+    mean: optionally two fp32 scalar tensors that receive the mean loss over
+    the rows with an entry and one over their number."""
     N, D, V = check_head(E, C)
     K, dtype = _check_targets(ids, teacher, N, E.device)
     with Launch(E.device, stream, workspace) as run:
@@ -108,19 +114,26 @@ def distill_forward(E, C, ids, teacher, temperature: float = 1.0, ignore_index: 
             loss, lse = out
             check_tensor(loss, "loss", (N,), torch.float32, E.device)
             check_tensor(lse, "lse", (N,), torch.float32, E.device)
+        means = (0, 0)
+        if mean is not None:
+            for t in mean:
+                check_tensor(t, "mean", (), torch.float32, E.device)
+            means = (mean[0].data_ptr(), mean[1].data_ptr())
         ws = run.scratch(cce_distill_forward_workspace_size(N, D, V, K), "cce_distill_forward_workspace_size")
         cce_distill_forward(E.data_ptr(), C.data_ptr(), ids.data_ptr(), teacher.data_ptr(), dtype, N, D, V, K,
-                            ignore_index, float(temperature), loss.data_ptr(), lse.data_ptr(), ws.data_ptr(),
-                            ws.numel(), run.ptr)
+                            ignore_index, float(temperature), loss.data_ptr(), lse.data_ptr(), *means,
+                            ws.data_ptr(), ws.numel(), run.ptr)
     return loss, lse
 
 
 def distill_backward(E, C, ids, teacher, lse, dloss, temperature: float = 1.0, ignore_index: int = IGNORE_INDEX,
                      workspace: Optional[Workspace] = None, stream=None, out=None, deterministic: bool = False,
-                     bf16_grads: bool = False, accumulate: bool = False):
+                     bf16_grads: bool = False, accumulate: bool = False, dloss_scale=None):
     """dE [N, D] and dC [V, D] of sum_i dloss[i] * loss[i] for the loss of
     distill_forward (every entry of the softmax's gradient; no filter): fp32,
-    or bf16 with bf16_grads.  deterministic=True sums dE in a fixed order;
+    or bf16 with bf16_grads.  dloss is [N], or a scalar tensor for all rows;
+    dloss_scale, a scalar tensor, multiplies it (with distill_forward's second
+    mean: the gradient of dloss times the mean).  deterministic=True sums dE in a fixed order;
     accumulate=True adds to the tensors given in `out` (required).  The
     logits are formed again on chip; the scratch is about 24 KB per token (at
     most ~400 MB), plus the fp32 sums of dE for bf16 outputs (and of dC with
@@ -128,7 +141,9 @@ def distill_backward(E, C, ids, teacher, lse, dloss, temperature: float = 1.0, i
     N, D, V = check_head(E, C)
     K, dtype = _check_targets(ids, teacher, N, E.device)
     check_tensor(lse, "lse", (N,), torch.float32, E.device)
-    check_tensor(dloss, "dloss", (N,), torch.float32, E.device)
+    check_tensor(dloss, "dloss", (N,) if dloss.dim() else (), torch.float32, E.device)
+    if dloss_scale is not None:
+        check_tensor(dloss_scale, "dloss_scale", (), torch.float32, E.device)
     if accumulate and out is None:
         raise ValueError("accumulate=True adds into existing gradients: pass them as out=(dE, dC)")
     flags = ((CCE_BWD_DETERMINISTIC if deterministic else 0) | (CCE_BWD_BF16_GRADS if bf16_grads else 0) |
@@ -143,6 +158,7 @@ def distill_backward(E, C, ids, teacher, lse, dloss, temperature: float = 1.0, i
             check_tensor(dC, "dC", (V, D), gdt, E.device)
         ws = run.scratch(cce_distill_backward_workspace_size(N, D, V, K, flags), "cce_distill_backward_workspace_size")
         cce_distill_backward(E.data_ptr(), C.data_ptr(), ids.data_ptr(), teacher.data_ptr(), dtype, lse.data_ptr(),
-                             dloss.data_ptr(), N, D, V, K, ignore_index, float(temperature), flags, dE.data_ptr(),
+                             dloss.data_ptr(), 1 if dloss.dim() else 0,
+                             0 if dloss_scale is None else dloss_scale.data_ptr(), N, D, V, K, ignore_index, float(temperature), flags, dE.data_ptr(),
                              dC.data_ptr(), ws.data_ptr(), ws.numel(), run.ptr)
     return dE, dC

@@ -80,10 +80,10 @@ def load_library():
         lib.cce_distill_backward_workspace_size.argtypes = [c_i64] * 4 + [ctypes.c_uint]
         lib.cce_distill_backward_workspace_size.restype = c_size
         lib.cce_distill_forward.argtypes = [c_vp, c_vp, c_vp, c_vp, ctypes.c_int, c_i64, c_i64, c_i64, c_i64, c_i64,
-                                            c_f32, c_vp, c_vp, c_vp, c_size, c_vp]
+                                            c_f32, c_vp, c_vp, c_vp, c_vp, c_vp, c_size, c_vp]
         lib.cce_distill_forward.restype = ctypes.c_int
-        lib.cce_distill_backward.argtypes = [c_vp, c_vp, c_vp, c_vp, ctypes.c_int, c_vp, c_vp, c_i64, c_i64, c_i64,
-                                             c_i64, c_i64, c_f32, ctypes.c_uint, c_vp, c_vp, c_vp, c_size, c_vp]
+        lib.cce_distill_backward.argtypes = [c_vp, c_vp, c_vp, c_vp, ctypes.c_int, c_vp, c_vp, ctypes.c_int, c_vp,
+                                             c_i64, c_i64, c_i64, c_i64, c_i64, c_f32, ctypes.c_uint, c_vp, c_vp, c_vp, c_size, c_vp]
         lib.cce_distill_backward.restype = ctypes.c_int
         lib.cce_head_workspace_size.argtypes = [c_i64] * 3
         lib.cce_head_workspace_size.restype = c_size
@@ -278,20 +278,22 @@ def cce_distill_backward_workspace_size(N: int, D: int, V: int, K: int, flags: i
 
 
 def cce_distill_forward(E: int, C: int, ids: int, teacher: int, teacher_dtype: int, N: int, D: int, V: int, K: int,
-                        ignore_index: int, temperature: float, loss: int, lse: int, workspace: int,
-                        workspace_bytes: int, stream: int, check: bool = True) -> int:
+                        ignore_index: int, temperature: float, loss: int, lse: int, mean: int, inv_count: int,
+                        workspace: int, workspace_bytes: int, stream: int, check: bool = True) -> int:
     st = load_library().cce_distill_forward(E, C, ids, teacher, teacher_dtype, N, D, V, K, ignore_index, temperature,
-                                            loss, lse, workspace, workspace_bytes, stream)
+                                            loss, lse, mean, inv_count, workspace, workspace_bytes, stream)
     if check:
         _check(st, "cce_distill_forward")
     return st
 
 
-def cce_distill_backward(E: int, C: int, ids: int, teacher: int, teacher_dtype: int, lse: int, dloss: int, N: int,
-                         D: int, V: int, K: int, ignore_index: int, temperature: float, flags: int, dE: int, dC: int,
-                         workspace: int, workspace_bytes: int, stream: int, check: bool = True) -> int:
-    st = load_library().cce_distill_backward(E, C, ids, teacher, teacher_dtype, lse, dloss, N, D, V, K, ignore_index,
-                                             temperature, flags, dE, dC, workspace, workspace_bytes, stream)
+def cce_distill_backward(E: int, C: int, ids: int, teacher: int, teacher_dtype: int, lse: int, dloss: int,
+                         dloss_stride: int, dloss_scale: int, N: int, D: int, V: int, K: int, ignore_index: int,
+                         temperature: float, flags: int, dE: int, dC: int, workspace: int, workspace_bytes: int,
+                         stream: int, check: bool = True) -> int:
+    st = load_library().cce_distill_backward(E, C, ids, teacher, teacher_dtype, lse, dloss, dloss_stride, dloss_scale,
+                                             N, D, V, K, ignore_index, temperature, flags, dE, dC, workspace,
+                                             workspace_bytes, stream)
     if check:
         _check(st, "cce_distill_backward")
     return st

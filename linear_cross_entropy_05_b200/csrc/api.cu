@@ -304,15 +304,28 @@ struct StripeLayout {
   size_t n_doneA_v, n_doneA_ms, n_doneBC, n_doneC, n_nz;
 };
 
-StripeLayout plan_stripes(int64_t N, int64_t D, int64_t V, size_t base) {
+// narrow_pairs > 0 (distillation): where whole stripes would leave fewer dE-tile
+// tasks than that many CTA pairs, narrower ones with as many buffers as their
+// columns allow, so that these tasks run side by side.  256 tokens x 256 x
+// 4096: one task over 4096 columns takes 32 of 48 us; 21 us in all with stripes of 256.
+StripeLayout plan_stripes(int64_t N, int64_t D, int64_t V, size_t base, int narrow_pairs = 0) {
   StripeLayout L{};
   const int n_m2_total = (int)((N + 255) / 256);
   L.p.n_m2 = std::min(n_m2_total, kStripeMaxM2);
   L.p.n_vtile = (int)((V + BN - 1) / BN);
   L.p.n_dc = (int)((D + 255) / 256);
   L.p.vt_per_s = std::min(L.p.n_vtile, g_stripe_vt.load());
+  int buffers = kStripeBuffers;
+  if (narrow_pairs > 0) {
+    const int64_t tiles = (int64_t)L.p.n_m2 * L.p.n_dc;
+    const int64_t fit = std::max<int64_t>(1, L.p.n_vtile * tiles / narrow_pairs);
+    if (fit < L.p.vt_per_s) {
+      buffers = kStripeBuffers * L.p.vt_per_s / (int)fit;
+      L.p.vt_per_s = (int)fit;
+    }
+  }
   L.p.n_s = (L.p.n_vtile + L.p.vt_per_s - 1) / L.p.vt_per_s;
-  L.p.nbuf = std::min(L.p.n_s, kStripeBuffers);
+  L.p.nbuf = std::min(L.p.n_s, buffers);
   L.p.order = g_stripe_order.load();
   L.p.gm = g_stripe_gm.load();
   L.p.lag = g_stripe_lag.load();
@@ -391,6 +404,8 @@ struct TargetBuffers {
   float* neg_entropy;
   int* row_kind;
   int K;
+  int dloss_stride;          // backward
+  const float* dloss_scale;
 };
 
 // The logit pass of the forward: launches the tile kernel, which leaves the
@@ -703,6 +718,8 @@ cce_status_t backward_stripes(const void* E, const void* C, void* dE, void* dC, 
     sa.row_kind = tg->row_kind;
     sa.scale2 = LOG2E / temperature;
     sa.temperature = temperature;
+    sa.dloss_stride = tg->dloss_stride;
+    sa.dloss_scale = tg->dloss_scale;
     sa.dC_bf16 = dC_bf16 ? 1 : 0;
   }
   sa.ordered = ordered ? 1 : 0;
@@ -1053,6 +1070,7 @@ bool plan_distill_forward(int64_t N, int64_t D, int64_t V, int64_t K, DistillLay
   return true;
 }
 
+constexpr int kNarrowPairs = 74;  // CTA pairs of a B200 (the workspace size does not depend on the device)
 constexpr unsigned kDistillFlags = CCE_BWD_DETERMINISTIC | CCE_BWD_BF16_GRADS | CCE_BWD_ACCUMULATE;
 
 bool plan_distill_backward(int64_t N, int64_t D, int64_t V, int64_t K, unsigned flags, DistillLayout* L) {
@@ -1073,7 +1091,7 @@ bool plan_distill_backward(int64_t N, int64_t D, int64_t V, int64_t K, unsigned 
       L->bytes += align_up((size_t)V * D * 4, 256);
     }
   }
-  L->stripes = plan_stripes(N, D, V, L->bytes);
+  L->stripes = plan_stripes(N, D, V, L->bytes, kNarrowPairs);
   L->bytes = L->stripes.bytes;
   return true;
 }
@@ -1121,13 +1139,15 @@ size_t cce_distill_backward_workspace_size(int64_t N, int64_t D, int64_t V, int6
 
 cce_status_t cce_distill_forward(const void* E, const void* C, const int64_t* ids, const void* teacher,
                                  int teacher_dtype, int64_t N, int64_t D, int64_t V, int64_t K, int64_t ignore_index,
-                                 float temperature, float* loss, float* lse, void* workspace, size_t workspace_bytes,
-                                 void* stream_) {
+                                 float temperature, float* loss, float* lse, float* mean, float* inv_count,
+                                 void* workspace, size_t workspace_bytes, void* stream_) {
   if (!E || !C || !ids || !teacher || !loss || !lse || !workspace) return CCE_ERR_INVALID_ARG;
+  if ((mean == nullptr) != (inv_count == nullptr)) return CCE_ERR_INVALID_ARG;
   if (!distill_sizes_ok(N, D, V, K) || !temperature_ok(temperature)) return CCE_ERR_INVALID_ARG;
   if (teacher_dtype != CCE_DTYPE_F32 && teacher_dtype != CCE_DTYPE_BF16) return CCE_ERR_INVALID_ARG;
   if (!aligned(E, 16) || !aligned(C, 16) || !aligned(ids, 8) || !aligned(loss, 4) || !aligned(lse, 4) ||
-      !aligned(teacher, teacher_dtype == CCE_DTYPE_BF16 ? 2 : 4) || !aligned(workspace, 256))
+      !aligned(teacher, teacher_dtype == CCE_DTYPE_BF16 ? 2 : 4) || !aligned(mean, 4) || !aligned(inv_count, 4) ||
+      !aligned(workspace, 256))
     return CCE_ERR_MISALIGNED;
   if (!device_info().ok) return CCE_ERR_UNSUPPORTED_DEVICE;
   DistillLayout L{};
@@ -1136,7 +1156,7 @@ cce_status_t cce_distill_forward(const void* E, const void* C, const int64_t* id
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   char* ws = reinterpret_cast<char*>(workspace);
   if (cudaMemsetAsync(ws, 0, STATUS_BYTES, stream) != cudaSuccess) return CCE_ERR_CUDA;
-  TargetBuffers tg;
+  TargetBuffers tg{};
   cce_status_t st = prepare_targets(ids, teacher, teacher_dtype, N, V, K, ignore_index, temperature, ws, L, &tg, stream);
   if (st != CCE_OK) return st;
   float* dot = reinterpret_cast<float*>(ws + L.off_dot);
@@ -1150,23 +1170,27 @@ cce_status_t cce_distill_forward(const void* E, const void* C, const int64_t* id
   f.dot = dot;
   f.neg_entropy = tg.neg_entropy;
   f.row_kind = tg.row_kind;
-  f.status = reinterpret_cast<const unsigned long long*>(ws);
+  f.status = reinterpret_cast<unsigned long long*>(ws);
   f.loss = loss;
   f.lse = lse;
+  f.mean = mean;
+  f.inv_count = inv_count;
   return launch_distill_finalize(f, stream) == cudaSuccess ? CCE_OK : CCE_ERR_CUDA;
 }
 
 cce_status_t cce_distill_backward(const void* E, const void* C, const int64_t* ids, const void* teacher,
-                                  int teacher_dtype, const float* lse, const float* dloss, int64_t N, int64_t D,
-                                  int64_t V, int64_t K, int64_t ignore_index, float temperature, unsigned flags,
-                                  void* dE, void* dC, void* workspace, size_t workspace_bytes, void* stream_) {
+                                  int teacher_dtype, const float* lse, const float* dloss, int dloss_stride,
+                                  const float* dloss_scale, int64_t N, int64_t D, int64_t V, int64_t K,
+                                  int64_t ignore_index, float temperature, unsigned flags, void* dE, void* dC,
+                                  void* workspace, size_t workspace_bytes, void* stream_) {
   if (!E || !C || !ids || !teacher || !lse || !dloss || !dE || !dC || !workspace) return CCE_ERR_INVALID_ARG;
+  if (dloss_stride != 0 && dloss_stride != 1) return CCE_ERR_INVALID_ARG;
   if (!distill_sizes_ok(N, D, V, K) || !temperature_ok(temperature)) return CCE_ERR_INVALID_ARG;
   if (teacher_dtype != CCE_DTYPE_F32 && teacher_dtype != CCE_DTYPE_BF16) return CCE_ERR_INVALID_ARG;
   if (flags & ~kDistillFlags) return CCE_ERR_INVALID_ARG;
   if (!aligned(E, 16) || !aligned(C, 16) || !aligned(ids, 8) || !aligned(lse, 4) || !aligned(dloss, 4) ||
       !aligned(teacher, teacher_dtype == CCE_DTYPE_BF16 ? 2 : 4) || !aligned(dE, 16) || !aligned(dC, 16) ||
-      !aligned(workspace, 256))
+      !aligned(dloss_scale, 4) || !aligned(workspace, 256))
     return CCE_ERR_MISALIGNED;
   DistillLayout L{};
   if (!plan_distill_backward(N, D, V, K, flags, &L)) return CCE_ERR_INVALID_ARG;
@@ -1176,7 +1200,7 @@ cce_status_t cce_distill_backward(const void* E, const void* C, const int64_t* i
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   char* ws = reinterpret_cast<char*>(workspace);
   if (cudaMemsetAsync(ws, 0, STATUS_BYTES, stream) != cudaSuccess) return CCE_ERR_CUDA;
-  TargetBuffers tg;
+  TargetBuffers tg{};
   cce_status_t st = prepare_targets(ids, teacher, teacher_dtype, N, V, K, ignore_index, temperature, ws, L, &tg, stream);
   if (st != CCE_OK) return st;
 
@@ -1201,6 +1225,8 @@ cce_status_t cce_distill_backward(const void* E, const void* C, const int64_t* i
   a.withhold_loads = g_withhold_loads.load();
   a.trace = g_bwd_trace.load();
   a.trace_cap = g_bwd_trace_cap.load();
+  tg.dloss_stride = dloss_stride;
+  tg.dloss_scale = dloss_scale;
   st = backward_stripes(E, C, dE32, dC_sum, bp, a, acc32, (flags & CCE_BWD_DETERMINISTIC) != 0, di.sms, ws, stream,
                         nullptr, &tg, temperature, L.dC_direct);
   if (st != CCE_OK || !bf16) return st;

@@ -549,7 +549,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SP_THREADS, 1)
           }
         }
         const float lse2 = valid ? a.lse[row] * LOG2E : 0.f;
-        const float dl = valid ? (PICK ? a.dloss[row] * a.temperature : a.dloss[row]) : 0.f;
+        float dl = 0.f;
+        if (valid) {
+          dl = a.dloss[PICK ? (size_t)row * a.dloss_stride : (size_t)row];
+          if constexpr (PICK) dl *= a.temperature * (a.dloss_scale ? *a.dloss_scale : 1.f);
+        }
         const long long yrel = yl - (long long)t.b * BN;
         const int ycol = (valid && yrel >= 0 && yrel < BN) ? (int)yrel : -1;
         const int ncols = min(BN, a.V - t.b * BN);

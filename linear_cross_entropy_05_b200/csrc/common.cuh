@@ -120,9 +120,13 @@ struct DistillFinArgs {
   const float* dot;          // [n_split][N]
   const float* neg_entropy;  // [N]
   const int* row_kind;       // [N]
-  const unsigned long long* status;
+  unsigned long long* status;  // (word ST_NEXT_TILE counts finished blocks)
   float* loss;
   float* lse;
+  // optional, both or neither: the mean of loss over the rows with a target,
+  // and one over their number
+  float* mean;
+  float* inv_count;
 };
 
 // The head's logits of a chunk of tokens and the choice among them (head.cu).
@@ -439,6 +443,8 @@ struct StripeArgs {
   const int* row_kind;
   float scale2;          // log2(e) / temperature
   float temperature;     // G = dloss * temperature * (softmax - targets)
+  int dloss_stride;      // 1, or 0: one dloss for all rows
+  const float* dloss_scale;  // optional: a factor of every dloss
   int dC_bf16;           // 1: dC-tile tasks store bf16 (dC_add = 0; the dC map is of bf16 boxes)
 };
 

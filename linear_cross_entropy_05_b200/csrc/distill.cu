@@ -15,7 +15,8 @@
 //                  the vocabulary in order, meet them one after another.
 // distill_finalize merges the splits' (max, sum, weighted logits) into lse
 //                  and loss; 32 rows x 8 split lanes per block, so the
-//                  [split][row] partials are read in whole lines.
+//                  [split][row] partials are read in whole lines.  The block
+//                  that finishes last adds up the mean, in a fixed order.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -34,11 +35,12 @@ __device__ __forceinline__ double block_reduce(double v, double* buf) {
     const double u = __shfl_xor_sync(0xffffffffu, v, o);
     v = MAX ? fmax(v, u) : v + u;
   }
+  const int tid = threadIdx.y * blockDim.x + threadIdx.x;
   __syncthreads();  // buf may still be read from an earlier reduction
-  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
+  if ((tid & 31) == 0) buf[tid >> 5] = v;
   __syncthreads();
   double r = buf[0];
-  for (int i = 1; i < (int)(blockDim.x >> 5); ++i) r = MAX ? fmax(r, buf[i]) : r + buf[i];
+  for (int i = 1; i < (int)(blockDim.x * blockDim.y >> 5); ++i) r = MAX ? fmax(r, buf[i]) : r + buf[i];
   return r;
 }
 
@@ -133,6 +135,7 @@ __global__ void __launch_bounds__(256) distill_finalize_kernel(const DistillFinA
   __shared__ float sm[8][32];
   __shared__ float ss[8][32];
   __shared__ double sd[8][32];
+  __shared__ int s_last;
   const int lane = threadIdx.x, part = threadIdx.y;
   const int row = blockIdx.x * 32 + lane;
   const float scale2 = LOG2E / a.temperature;
@@ -151,26 +154,51 @@ __global__ void __launch_bounds__(256) distill_finalize_kernel(const DistillFinA
   ss[part][lane] = s;
   sd[part][lane] = dot;
   __syncthreads();
-  if (part != 0 || row >= a.N) return;
-  for (int q = 1; q < 8; ++q) M = fmaxf(M, sm[q][lane]);
-  s = 0.f;
-  dot = 0.0;
-  for (int q = 0; q < 8; ++q) {
-    if (sm[q][lane] != -INFINITY) s += ss[q][lane] * exp2f((sm[q][lane] - M) * scale2);
-    dot += sd[q][lane];
+  if (part == 0 && row < a.N) {
+    for (int q = 1; q < 8; ++q) M = fmaxf(M, sm[q][lane]);
+    s = 0.f;
+    dot = 0.0;
+    for (int q = 0; q < 8; ++q) {
+      if (sm[q][lane] != -INFINITY) s += ss[q][lane] * exp2f((sm[q][lane] - M) * scale2);
+      dot += sd[q][lane];
+    }
+    const double T = (double)a.temperature;
+    const double L = (double)M / T + log((double)s);
+    const int kind = a.row_kind[row];
+    double loss = 0.0;
+    if (kind == ROW_LIVE)
+      loss = T * T * ((double)a.neg_entropy[row] - dot / T + L);
+    float lse = (float)L, out = (float)loss;
+    if (kind == ROW_BAD) out = __int_as_float(0x7fc00000);
+    // a bounded wait gave up: some partials may be an earlier call's
+    if (a.status[ST_FLAGS] & SF_TIMEOUT) lse = out = __int_as_float(0x7fc00000);
+    a.lse[row] = lse;
+    a.loss[row] = out;
   }
-  const double T = (double)a.temperature;
-  const double L = (double)M / T + log((double)s);
-  const int kind = a.row_kind[row];
-  double loss = 0.0;
-  if (kind == ROW_LIVE)
-    loss = T * T * ((double)a.neg_entropy[row] - dot / T + L);
-  float lse = (float)L, out = (float)loss;
-  if (kind == ROW_BAD) out = __int_as_float(0x7fc00000);
-  // a bounded wait gave up: some partials may be an earlier call's
-  if (a.status[ST_FLAGS] & SF_TIMEOUT) lse = out = __int_as_float(0x7fc00000);
-  a.lse[row] = lse;
-  a.loss[row] = out;
+  if (!a.mean) return;
+
+  // the mean, by the last block to get here
+  __threadfence();
+  __syncthreads();
+  const int tid = part * 32 + lane;
+  if (tid == 0) s_last = atomicAdd(a.status + ST_NEXT_TILE, 1ull) == gridDim.x - 1ull;
+  __syncthreads();
+  if (!s_last) return;
+  __threadfence();
+  double sum = 0.0, n = 0.0;
+  for (int i = tid; i < a.N; i += 256) {
+    if (a.row_kind[i] != ROW_EMPTY) {
+      sum += (double)__ldcg(a.loss + i);
+      n += 1.0;
+    }
+  }
+  double* buf = &sd[0][0];
+  sum = block_reduce<false>(sum, buf);
+  n = block_reduce<false>(n, buf);
+  if (tid == 0) {
+    *a.mean = (float)(sum / n);
+    *a.inv_count = (float)(1.0 / n);
+  }
 }
 
 cudaError_t launch_distill_targets(const TargetArgs& a, cudaStream_t stream) {

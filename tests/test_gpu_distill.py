@@ -208,6 +208,32 @@ def test_autograd_mean_over_rows_with_a_target():
     assert np.linalg.norm(E2.grad.double().cpu().numpy() - dE / 3) <= 2 * U16 * np.linalg.norm(dE / 3)
 
 
+def test_means_and_one_dloss_for_all_rows():
+    import torch
+    import linear_cross_entropy_05_b200 as L
+    for N, V in ((1, 50), (33, 300), (2100, 777)):
+        E, C, ids, t, _ = [x.cuda() for x in make(N, N, 64, V, 7)]
+        if N > 1:
+            ids[::3] = IGN
+        mean, inv = torch.zeros((), device="cuda"), torch.zeros((), device="cuda")
+        loss, lse = L.distill_forward(E, C, ids, t, mean=(mean, inv))
+        kept = (ids != IGN).any(1)
+        n = int(kept.sum())
+        # one rounding each of a double sum
+        assert inv.item() == float(np.float32(1.0 / n))
+        want = loss.double()[kept].sum().item() / n
+        assert abs(mean.item() - want) <= 1.01 * U32 * abs(want) + 1e-12
+        a = L.distill_backward(E, C, ids, t, lse, torch.tensor(0.7, device="cuda"), dloss_scale=inv, deterministic=True)
+        b = L.distill_backward(E, C, ids, t, lse, (0.7 * inv).expand(N).contiguous(), deterministic=True)
+        for p, q in zip(a, b):   # the factors are multiplied in another order: a last bit of G
+            assert (p - q).norm() <= U16 * q.norm()
+    ids[:] = IGN
+    E.requires_grad_()
+    out = L.linear_distillation(E, C, ids, t)
+    out.backward()
+    assert torch.isnan(out) and (E.grad == 0).all()
+
+
 def test_one_entry_at_temperature_one_is_the_cross_entropy():
     import torch
     import linear_cross_entropy_05_b200 as L
