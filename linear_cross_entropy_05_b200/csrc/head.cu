@@ -35,6 +35,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <cfloat>
+
 #include "common.cuh"
 #include "ptx.cuh"
 
@@ -410,7 +412,6 @@ struct SelectShared {
   };
   double tab[kExpTab];
   double red[HS_WARPS];
-  unsigned hist[256];
   unsigned ured[3][HS_WARPS];
   int rank[HS_THREADS];
   int count;
@@ -499,54 +500,8 @@ __device__ __forceinline__ double block_scan(double v, SelectShared& s, double& 
   return before + (lane ? ex : 0.0);
 }
 
-// The want-th largest key (want >= 1) of n keys given by key(i), by four
-// 8-bit digits; `rank` of them with that key belong to the want largest.
-template <typename KeyFn>
-__device__ unsigned radix_select(int n, int want, KeyFn key, SelectShared& s, int& rank) {
-  unsigned prefix = 0u, mask = 0u;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    __syncthreads();
-    for (int i = threadIdx.x; i < 256; i += HS_THREADS) s.hist[i] = 0u;
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += HS_THREADS) {
-      const unsigned k = key(i);
-      if ((k & mask) == prefix) atomicAdd(&s.hist[(k >> shift) & 255u], 1u);
-    }
-    __syncthreads();
-    if (threadIdx.x < 32) {
-      // lane l holds digits 255 - 8 l .. 248 - 8 l, largest first
-      unsigned part = 0u;
-      for (int j = 0; j < 8; ++j) part += s.hist[255 - 8 * threadIdx.x - j];
-      unsigned inc = part;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned u = __shfl_up_sync(0xffffffffu, inc, o);
-        if ((int)threadIdx.x >= o) inc += u;
-      }
-      unsigned before = inc - part;
-      if (before < (unsigned)want && (unsigned)want <= inc) {
-        for (int j = 0; j < 8; ++j) {
-          const unsigned h = s.hist[255 - 8 * threadIdx.x - j];
-          if ((unsigned)want <= before + h) {
-            s.found_key = 255u - 8u * threadIdx.x - (unsigned)j;
-            s.found_rank = want - (int)before;
-            break;
-          }
-          before += h;
-        }
-      }
-    }
-    __syncthreads();
-    prefix |= s.found_key << shift;
-    mask |= 255u << shift;
-    want = s.found_rank;
-  }
-  rank = want;
-  return prefix;
-}
-
 // A key that at least `want` bin maxima reach, and not many more: halving by
-// counting threads, until the number is within half of `want` or the keys are
+// counting threads, until the number is near `want` or the keys are
 // exhausted; 0 if fewer than 3 / 2 `want` threads have a bin that holds anything
 // (then the bound would be a poor one).  (A radix select's first digits put
 // every group into one bin: 8000 additions to one word a digit, 77 us for one
@@ -560,7 +515,7 @@ __device__ unsigned bin_threshold(const Row& r, int want, SelectShared& s) {
     const int c = __syncthreads_count(mine >= mid);
     if (c >= want) {
       lo = mid;
-      if (c <= want + want / 2 + 16) break;
+      if (c <= want + min(want / 2, 128) + 16) break;
     } else {
       hi = mid;
     }
@@ -574,7 +529,7 @@ __device__ unsigned bin_threshold(const Row& r, int want, SelectShared& s) {
 __device__ unsigned group_threshold(const Row& r, int want, SelectShared& s) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   unsigned lo = 0u, hi = r.top + 1u;
-  const int enough = want + want / 2 + 16;
+  const int enough = want + min(want / 2, 128) + 16;
   while (hi - lo > 1u) {
     const unsigned step = max(1u, (hi - lo) / 4u);
     const unsigned t1 = lo + step, t2 = min(hi, t1 + step), t3 = min(hi, t2 + step);
@@ -783,163 +738,255 @@ __device__ void sort_candidates(SelectShared& s, int n) {
 }
 __device__ __forceinline__ unsigned cand_key(unsigned long long c) { return ~(unsigned)(c >> 32); }
 
-// Appends, in the order of ids, the entries with key > kappa and the first
-// `ties` entries with key == kappa to s.cand (their number is at most kCap).
-__device__ int gather_exact(const Row& r, unsigned kappa, int ties, SelectShared& s) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  // ties before each warp's contiguous share of the groups
-  const int per = (r.n_grp + HS_WARPS - 1) / HS_WARPS;
-  const int ga = min(r.n_grp, w * per), gb = min(r.n_grp, ga + per);
-  int mine = 0;
-  for (int g = ga; g < gb; ++g) {
-    const int v = g * 32 + lane;
-    mine += __popc(__ballot_sync(0xffffffffu, v < r.V && order_key(__ldg(r.z + v)) == kappa));
+// ---- the whole row: where bins, groups and candidates do not settle it ----
+
+// f(id, logit) for the entries [a, b) of this warp, four loads at a time.
+template <typename F>
+__device__ __forceinline__ void warp_stream(const Row& r, int a, int b, F f) {
+  for (int v0 = a + (int)(threadIdx.x & 31); v0 < b; v0 += 128) {
+    float z[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) z[j] = v0 + 32 * j < b ? __ldg(r.z + v0 + 32 * j) : 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (v0 + 32 * j < b) f(v0 + 32 * j, z[j]);
   }
+}
+// A sixteenth of [a, b), in whole groups, rounded up.
+__device__ __forceinline__ int part_of(int a, int b) { return ((b - a) / HS_WARPS + 32) & ~31; }
+
+// Sum of weight(id, logit) over each warp's part of [a, b), to s.red.
+template <typename F>
+__device__ void part_sums(const Row& r, int a, int b, F weight, SelectShared& s) {
+  const int w = threadIdx.x >> 5, part = part_of(a, b);
+  double m = 0.0;
+  warp_stream(r, min(b, a + w * part), min(b, a + w * part + part), [&](int v, float z) { m += weight(v, z); });
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
   __syncthreads();
-  if (lane == 0) s.ured[0][w] = (unsigned)mine;
+  if ((threadIdx.x & 31) == 0) s.red[w] = m;
+  __syncthreads();
+}
+
+// The first id of [a, b) at which the cumulated weight is above `left` (the
+// last with any weight if none is); s.red holds part_sums of that range.
+template <typename F>
+__device__ int locate(const Row& r, int a, int b, double left, F weight, SelectShared& s) {
+  while (true) {
+    // the part that holds it: the last with any weight that begins at or below it
+    const int part = part_of(a, b);
+    int at = 0;
+    double run = 0.0, skipped = 0.0;
+    for (int i = 0; i < HS_WARPS; ++i) {
+      if (s.red[i] > 0.0 && run <= left) {
+        at = i;
+        skipped = run;
+      }
+      run += s.red[i];
+    }
+    left -= skipped;
+    a = min(b, a + at * part);
+    b = min(b, a + part);
+    if (b - a <= 256) break;
+    part_sums(r, a, b, weight, s);
+  }
+  const int lane = threadIdx.x & 31;
+  int last = a;
+  for (int v0 = a; v0 < b; v0 += 32) {  // (every warp alike)
+    const int v = v0 + lane;
+    const double own = v < b ? weight(v, __ldg(r.z + v)) : 0.0;
+    double inc = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    const unsigned any = __ballot_sync(0xffffffffu, own > 0.0);
+    const unsigned over = __ballot_sync(0xffffffffu, own > 0.0 && inc > left);
+    if (over) return v0 + __ffs((int)over) - 1;
+    if (any) last = v0 + 31 - __clz((int)any);
+    left -= __shfl_sync(0xffffffffu, inc, 31);
+  }
+  return last;
+}
+
+// A prefix of the falling order: the entries above `key` and those with that
+// key and an id up to `id`.
+struct Border {
+  unsigned key;
+  int id;
+};
+__device__ __forceinline__ bool within(const Border& e, unsigned key, int v) {
+  return key > e.key || (key == e.key && v <= e.id);
+}
+
+// Appends the entries of the row that take(id, key) accepts to s.cand; their
+// number (at most kCap are kept).
+template <typename F>
+__device__ int gather_if(const Row& r, F take, SelectShared& s) {
+  const int w = threadIdx.x >> 5, part = part_of(0, r.V);
+  __syncthreads();
   if (threadIdx.x == 0) s.count = 0;
   __syncthreads();
-  int seen = 0;
-  for (int i = 0; i < w; ++i) seen += (int)s.ured[0][i];
-  for (int g = ga; g < gb; ++g) {
-    const int v = g * 32 + lane;
-    const unsigned k = v < r.V ? order_key(__ldg(r.z + v)) : 0u;
-    const unsigned eq = __ballot_sync(0xffffffffu, v < r.V && k == kappa);
-    const bool hit = v < r.V && (k > kappa || (k == kappa && seen + __popc(eq & ((1u << lane) - 1u)) < ties));
-    const unsigned hits = __ballot_sync(0xffffffffu, hit);
-    if (hits) {
-      int base = 0;
-      if (lane == 0) base = atomicAdd(&s.count, __popc(hits));
-      base = __shfl_sync(0xffffffffu, base, 0);
-      const int at = base + __popc(hits & ((1u << lane) - 1u));
-      if (hit && at < kCap) s.cand[at] = ((unsigned long long)(~k) << 32) | (unsigned)v;
+  warp_stream(r, min(r.V, w * part), min(r.V, w * part + part), [&](int v, float z) {
+    const unsigned key = order_key(z);
+    if (take(v, key)) {
+      const int at = atomicAdd(&s.count, 1);
+      if (at < kCap) s.cand[at] = ((unsigned long long)(~key) << 32) | (unsigned)v;
     }
-    seen += __popc(eq);
-  }
+  });
   __syncthreads();
   return min(s.count, kCap);
+}
+
+// The shortest prefix that holds `need` (> 0) entries, or (MASS) `need` of the
+// mass sum exp((z - zmax) / T).  Three thresholds a pass close in on the key
+// where it ends, until at most kCap entries are left to sort, or one key.
+template <bool MASS>
+__device__ Border find_border(const Row& r, double need, SelectShared& s) {
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, part = part_of(0, r.V);
+  // measure(>= lo) >= need > measure(>= hi); so many entries reach either
+  unsigned lo = 0u, hi = r.top + 1u;
+  double above = 0.0;
+  int n_lo = r.V, n_hi = 0;
+  float reach = fmaxf(fmaxf(r.zmax - key_value(r.low), 1e-6f * fabsf(r.zmax)), 1e-30f);
+  for (int pass = 0; n_lo - n_hi > kCap && hi - lo > 1u; ++pass) {
+    unsigned t[3];  // rising
+    if (lo == 0u && pass < 16) {
+      // no lower end yet: steps from the largest that grow
+      const float z0 = pass == 0 ? r.zmax : key_value(hi);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) t[i] = order_key(fmaxf(z0 - reach * (i == 0 ? 4.f : i == 1 ? 2.f : 1.f), -FLT_MAX));
+      reach *= 8.f;
+    } else if (pass < 32) {
+      // quarters of the logits between them
+      const float a = key_value(lo), b = key_value(hi - 1u), d = b * 0.25f - a * 0.25f;
+#pragma unroll
+      for (int i = 0; i < 3; ++i) t[i] = order_key(a + d * (float)(i + 1));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 3; ++i) t[i] = lo + (unsigned)(((unsigned long long)(hi - lo) * (i + 1)) >> 2);
+    }
+#pragma unroll
+    for (int i = 0; i < 3; ++i) t[i] = min(max(t[i], lo + 1u), hi - 1u);
+    double m[3] = {0.0, 0.0, 0.0};
+    int c[3] = {0, 0, 0};
+    warp_stream(r, min(r.V, w * part), min(r.V, w * part + part), [&](int, float z) {
+      const unsigned key = order_key(z);
+      if (key >= t[0]) {
+        const double e = MASS ? mass_of(r, z) : 0.0;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          if (key >= t[i]) {
+            ++c[i];
+            if (MASS) m[i] += e;
+          }
+        }
+      }
+    });
+    int n[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      n[i] = __reduce_add_sync(0xffffffffu, c[i]);
+      __syncthreads();
+      if (lane == 0) s.ured[0][w] = (unsigned)n[i];
+      __syncthreads();
+      n[i] = (int)__reduce_add_sync(0xffffffffu, lane < HS_WARPS ? s.ured[0][lane] : 0u);
+      m[i] = MASS ? block_sum(m[i], s) : (double)n[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {  // (rising: the last that still holds it)
+      if (m[i] >= need && t[i] > lo) {
+        lo = t[i];
+        n_lo = n[i];
+      }
+    }
+#pragma unroll
+    for (int i = 2; i >= 0; --i) {
+      if (!(m[i] >= need) && t[i] < hi) {
+        hi = t[i];
+        n_hi = n[i];
+        above = m[i];
+      }
+    }
+  }
+  const int left = n_lo - n_hi;
+  if (left > kCap) {
+    // one key, of which the lowest ids belong to it
+    const double one = MASS ? mass_of(r, key_value(lo)) : 1.0;
+    const double want = ceil((need - above) / one);
+    const int n = want >= 1.0 ? (want < (double)left ? (int)want : left) : 1;
+    if (n == left) return Border{lo, r.V};
+    auto is_tie = [&](int, float z) { return order_key(z) == lo ? 1.0 : 0.0; };
+    part_sums(r, 0, r.V, is_tie, s);
+    return Border{lo, locate(r, 0, r.V, (double)n - 0.5, is_tie, s)};
+  }
+  const int c = gather_if(r, [&](int, unsigned key) { return key >= lo && key < hi; }, s);
+  sort_candidates(s, c);
+  // the entries before which less than `need` has come
+  constexpr int PER = kCap / HS_THREADS;
+  const int i0 = threadIdx.x * PER;
+  double e[PER], sum = 0.0, total;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    e[j] = i0 + j < c ? (MASS ? mass_of(r, key_value(cand_key(s.cand[i0 + j]))) : 1.0) : 0.0;
+    sum += e[j];
+  }
+  double before = above + block_scan(sum, s, total);
+  unsigned keep = 0u;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    if (i0 + j < c && before < need) keep = (unsigned)(i0 + j + 1);
+    before += e[j];
+  }
+  const int n = (int)block_pick<true>(keep, s);
+  if (n == 0) return Border{min(hi, r.top), r.V};  // (does not happen: `above` is less than `need`)
+  const unsigned long long last = s.cand[n - 1];
+  return Border{cand_key(last), (int)(unsigned)last};
 }
 
 // The k largest entries (k <= kCap, k <= V) as candidates: at least these,
 // sorted; their number.
 __device__ int top_candidates(const Row& r, int k, SelectShared& s) {
-  int c = kCap + 1, rank;
+  int c = kCap + 1;
   unsigned thr;
   if (r.n_grp >= k || r.V <= kCap) c = gather_top_groups(r, k, 0u, thr, s);
   if (c > kCap) {
-    thr = radix_select(r.V, k, [&](int v) { return order_key(__ldg(r.z + v)); }, s, rank);
-    c = gather_exact(r, thr, rank, s);
+    const Border e = find_border<false>(r, (double)k, s);
+    c = gather_if(r, [&](int v, unsigned key) { return within(e, key, v); }, s);
   }
   sort_candidates(s, c);
   return c;
 }
 
-// Sum of exp((z - zmax) / T) over the row's entries with key >= lo.
-__device__ double mass_from(const Row& r, unsigned lo, SelectShared& s) {
-  double m = 0.0;
-  for (int v = threadIdx.x; v < r.V; v += HS_THREADS) {
-    const float z = __ldg(r.z + v);
-    if (order_key(z) >= lo) m += mass_of(r, z);
-  }
-  return block_sum(m, s);
-}
-
-// Settles row-wide what the sorted candidates could not: the prefix, in
-// falling order, that top-k (k > 0), top-p and min-p leave, as a smallest key
-// and how many of the entries with that key belong to it (lowest ids first);
-// then the draw in the order of ids.
+// Settles row-wide what the sorted candidates could not: the prefix that top-k
+// (k > 0) and top-p leave, and the draw from it, in the order of ids, without
+// the entries below min_p.
 __device__ int wide_draw(const Row& r, int k, double p, double min_p, double u, double total, SelectShared& s) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  unsigned kappa = 0u;
-  int ties = r.V;
-  auto row_key = [&](int v) { return order_key(__ldg(r.z + v)); };
-  if (k > 0 && k < r.V) {
-    kappa = radix_select(r.V, k, row_key, s, ties);
-    total = mass_from(r, kappa + 1u, s) + ties * mass_of(r, key_value(kappa));
+  Border e{0u, r.V};
+  auto kept = [&](int v, float z) {
+    if (!within(e, order_key(z), v)) return 0.0;
+    const double m = mass_of(r, z);
+    return m >= min_p ? m : 0.0;
+  };
+  auto sum_parts = [&]() {
+    double t = 0.0;
+    for (int i = 0; i < HS_WARPS; ++i) t += s.red[i];
+    return t;
+  };
+  if (k > 0) {
+    e = find_border<false>(r, (double)k, s);
+    if (p < 1.0) {
+      part_sums(r, 0, r.V, [&](int v, float z) { return within(e, order_key(z), v) ? mass_of(r, z) : 0.0; }, s);
+      total = sum_parts();
+    }
   }
   if (p < 1.0) {
-    // the largest key whose entries and those above it hold p of the mass,
-    // one bit at a time from the top (never below kappa)
-    const double need = p * total;
-    unsigned key = 0u;
-    for (int bit = 31; bit >= 0; --bit) {
-      const unsigned t = key | (1u << bit);
-      if (t <= kappa || (t <= order_key(r.zmax) && mass_from(r, t, s) >= need)) key = t;
-    }
-    const double above = mass_from(r, key + 1u, s);
-    const double one = mass_of(r, key_value(key));
-    const double left = ceil((need - above) / one);
-    const int n = left < 1.0 ? 1 : (left > (double)r.V ? r.V : (int)left);
-    ties = key == kappa ? min(ties, n) : n;
-    kappa = max(key, kappa);
+    const Border q = find_border<true>(r, fmax(p * total, 1e-300), s);
+    if (q.key > e.key || (q.key == e.key && q.id < e.id)) e = q;
   }
-  // min-p leaves a prefix of it too: an entry's own mass decides
-  auto kept = [&](unsigned key, float z, int tie) {
-    return key > kappa || (key == kappa && tie < ties) ? mass_of(r, z) : 0.0;
-  };
-  const int per = (r.n_grp + HS_WARPS - 1) / HS_WARPS;
-  const int ga = min(r.n_grp, w * per), gb = min(r.n_grp, ga + per);
-  int mine = 0;
-  for (int g = ga; g < gb; ++g) {
-    const int v = g * 32 + lane;
-    mine += __popc(__ballot_sync(0xffffffffu, v < r.V && row_key(v) == kappa));
-  }
-  __syncthreads();
-  if (lane == 0) s.ured[0][w] = (unsigned)mine;
-  __syncthreads();
-  int seen0 = 0;
-  for (int i = 0; i < w; ++i) seen0 += (int)s.ured[0][i];
-  // this lane's kept mass of group g
-  auto group_mass = [&](int g, int& seen) {
-    const int v = g * 32 + lane;
-    const float z = v < r.V ? __ldg(r.z + v) : 0.f;
-    const unsigned key = v < r.V ? order_key(z) : 0u;
-    const unsigned eq = __ballot_sync(0xffffffffu, v < r.V && key == kappa);
-    double e = v < r.V ? kept(key, z, seen + __popc(eq & ((1u << lane) - 1u))) : 0.0;
-    if (e < min_p) e = 0.0;
-    seen += __popc(eq);
-    return e;
-  };
-  double m = 0.0;
-  int seen = seen0;
-  for (int g = ga; g < gb; ++g) m += group_mass(g, seen);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
-  __syncthreads();
-  if (lane == 0) s.red[w] = m;
-  if (threadIdx.x == 0) s.out_i = -1;
-  __syncthreads();
-  double before = 0.0, all = 0.0;
-  int last_warp = 0;
-  for (int i = 0; i < HS_WARPS; ++i) {
-    if (i < w) before += s.red[i];
-    all += s.red[i];
-    if (s.red[i] > 0.0) last_warp = i;
-  }
-  const double target = u * all;
-  const bool here = m > 0.0 && before <= target && (target < before + m || w == last_warp);
-  const bool fallback = w == last_warp && !(target < all);
-  if (here || fallback) {
-    double run = before;
-    int pick = -1, last = -1;
-    seen = seen0;
-    for (int g = ga; g < gb && pick < 0; ++g) {
-      double e = group_mass(g, seen);
-      const unsigned any = __ballot_sync(0xffffffffu, e > 0.0);
-      if (any) last = g * 32 + 31 - __clz((int)any);
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double x = __shfl_up_sync(0xffffffffu, e, o);
-        if (lane >= o) e += x;
-      }
-      const unsigned over = __ballot_sync(0xffffffffu, run + e > target) & any;
-      if (over) pick = g * 32 + __ffs((int)over) - 1;
-      run += __shfl_sync(0xffffffffu, e, 31);
-    }
-    if (lane == 0) s.out_i = pick >= 0 ? pick : last;
-  }
-  __syncthreads();
-  return s.out_i;
+  part_sums(r, 0, r.V, kept, s);
+  return locate(r, 0, r.V, u * sum_parts(), kept, s);
 }
 
 // Draw without filters: the first id whose cumulated mass passes u times the

@@ -123,11 +123,12 @@ def test_draws_match_the_definition(N, D, V):
     check_draw(L.sample(E.cuda(), C.cuda(), u.cuda(), workspace=ws, **dev), z, u, rows)
 
 
+@pytest.mark.parametrize("V,spread", [(20000, 0.5), (70001, 2.5)])
 @pytest.mark.parametrize("coarse", [False, True])
-def test_wide_prefixes_and_rows_full_of_ties(coarse):
+def test_wide_prefixes_and_rows_full_of_ties(coarse, V, spread):
     """Kept sets of more entries than the sorted ones, and ties across every border."""
     import linear_cross_entropy_05_b200 as L
-    E, C, z, u = make(8, 12, 32, 20000, spread=0.5, coarse=coarse)
+    E, C, z, u = make(8, 12, 32, V, spread=spread, coarse=coarse)
     E[3] = 0
     E[4] = 0
     E[5] = 0
@@ -135,7 +136,8 @@ def test_wide_prefixes_and_rows_full_of_ties(coarse):
     u[3], u[4], u[5] = 0.0, 0.5, 1.0 - 2.0 ** -24
     for s in (dict(top_p=0.9), dict(top_k=6000), dict(top_k=6000, top_p=0.8), dict(min_p=0.2), dict(top_p=0.7, min_p=0.3),
               dict(top_k=7001, top_p=0.95, min_p=0.1, temperature=1.25), dict(top_k=50), dict(), dict(temperature=0.0),
-              dict(top_p=0.01), dict(top_p=1.0 - 2.0 ** -24)):
+              dict(top_p=0.01), dict(top_p=1.0 - 2.0 ** -24), dict(top_p=0.6, temperature=50.0), dict(top_k=4097),
+              dict(top_k=V - 1, top_p=0.99), dict(top_p=0.97, temperature=3.0, min_p=1e-5)):
         check_draw(L.sample(E.cuda(), C.cuda(), u.cuda(), **s), z, u, s)
 
 
