@@ -305,9 +305,13 @@ struct StripeLayout {
 };
 
 // narrow_pairs > 0 (distillation): where whole stripes would leave fewer dE-tile
-// tasks than that many CTA pairs, narrower ones with as many buffers as their
-// columns allow, so that these tasks run side by side.  256 tokens x 256 x
-// 4096: one task over 4096 columns takes 32 of 48 us; 21 us in all with stripes of 256.
+// tasks than that many CTA pairs, narrower ones, so that these tasks run side
+// by side (256 tokens x 256 x 4096: one task over 4096 columns takes 32 of
+// 48 us; 21 us in all with stripes of 256); and as many buffers as kStripeRoom
+// holds, so that a few tokens' stripes, whose tasks do not fill the GPU, do not
+// wait for one another (6 tokens x 744 x 180434: 802 us with three buffers,
+// WIDE us with all 45).
+constexpr size_t kStripeRoom = size_t(128) << 20;
 StripeLayout plan_stripes(int64_t N, int64_t D, int64_t V, size_t base, int narrow_pairs = 0) {
   StripeLayout L{};
   const int n_m2_total = (int)((N + 255) / 256);
@@ -315,17 +319,14 @@ StripeLayout plan_stripes(int64_t N, int64_t D, int64_t V, size_t base, int narr
   L.p.n_vtile = (int)((V + BN - 1) / BN);
   L.p.n_dc = (int)((D + 255) / 256);
   L.p.vt_per_s = std::min(L.p.n_vtile, g_stripe_vt.load());
-  int buffers = kStripeBuffers;
+  int64_t buffers = kStripeBuffers;
   if (narrow_pairs > 0) {
-    const int64_t tiles = (int64_t)L.p.n_m2 * L.p.n_dc;
-    const int64_t fit = std::max<int64_t>(1, L.p.n_vtile * tiles / narrow_pairs);
-    if (fit < L.p.vt_per_s) {
-      buffers = kStripeBuffers * L.p.vt_per_s / (int)fit;
-      L.p.vt_per_s = (int)fit;
-    }
+    const int64_t fit = std::max<int64_t>(1, (int64_t)L.p.n_vtile * L.p.n_m2 * L.p.n_dc / narrow_pairs);
+    L.p.vt_per_s = (int)std::min<int64_t>(L.p.vt_per_s, fit);
+    buffers = std::max<int64_t>(buffers, (int64_t)(kStripeRoom / ((size_t)L.p.n_m2 * 256 * L.p.vt_per_s * BN * 2)));
   }
   L.p.n_s = (L.p.n_vtile + L.p.vt_per_s - 1) / L.p.vt_per_s;
-  L.p.nbuf = std::min(L.p.n_s, buffers);
+  L.p.nbuf = (int)std::min<int64_t>(L.p.n_s, buffers);
   L.p.order = g_stripe_order.load();
   L.p.gm = g_stripe_gm.load();
   L.p.lag = g_stripe_lag.load();
