@@ -42,7 +42,7 @@
 // memory.  Roles per CTA (320 threads): warp 0 TMA producer, warp 1 UMMA
 // issuer (leader CTA only), warps 2-9 epilogue (two per TMEM lane group, one
 // per 128-column half).  Each CTA stages 32 KB of
-// operands per 64-wide K slice (5 stages) and double-buffers a 128 x 256 fp32
+// operands per 64-wide K slice (5 stages; distillation 6) and double-buffers a 128 x 256 fp32
 // accumulator in TMEM, so the epilogue of one task overlaps the MMAs of the
 // next.  No TMA multicast: every load reads this GPU's memory.
 #include <cuda.h>
@@ -56,11 +56,15 @@ namespace cce {
 
 namespace {
 
-constexpr int SP_STAGES = 5;
+// Operand stages, and 4 KB staging boxes of an epilogue warp (bf16 G or fp32
+// blocks): of 227 KB either five and two, or six and one.
+template <bool PICK>
+constexpr int kStages = PICK ? 6 : 5;
+template <bool PICK>
+constexpr int kStagingBytes = PICK ? 4096 : 8192;
 constexpr int SP_STAGE_BYTES = 32768;          // per CTA: two 16 KB operand regions
 constexpr int SP_EPI_WARPS = 8;                // two per TMEM lane group, one per 128-column half
 constexpr int SP_THREADS = 64 + 32 * SP_EPI_WARPS;
-constexpr int SP_STAGING_PER_WARP = 8192;      // epilogue staging: two 4 KB boxes (bf16 G or fp32 blocks)
 constexpr int SP_RING = 4;                     // task hand-off slots
 constexpr int SP_CONSUMERS = 2 + 2 * SP_EPI_WARPS;  // leader: MMA + epilogue warps; peer: producer + epilogue warps
 constexpr unsigned SP_DONE = 2 * SP_EPI_WARPS; // completion arrivals per task (epilogue warps of both CTAs)
@@ -106,10 +110,12 @@ __device__ __forceinline__ void stage_f32_block(uint8_t* xb, int lane, const flo
 template <bool PICK>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SP_THREADS, 1)
     bwd_stripe_kernel(const __grid_constant__ StripeMaps mp, const StripeArgs a, __nv_bfloat16* G) {
+  constexpr int SP_STAGES = kStages<PICK>;
+  constexpr int SP_STAGING_PER_WARP = kStagingBytes<PICK>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* stages = smem;                                          // SP_STAGES x 32 KB
-  uint8_t* staging = smem + SP_STAGES * SP_STAGE_BYTES;            // SP_EPI_WARPS x 8 KB
+  uint8_t* staging = smem + SP_STAGES * SP_STAGE_BYTES;            // SP_EPI_WARPS x 4 or 8 KB
   uint64_t* bars = reinterpret_cast<uint64_t*>(staging + SP_EPI_WARPS * SP_STAGING_PER_WARP);
   uint64_t* full = bars;                          // leader: both CTAs' copies of a stage landed
   uint64_t* empty = bars + SP_STAGES;             // each CTA: stage free again
@@ -605,13 +611,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SP_THREADS, 1)
             pk[j >> 1] = pack_bf16x2(g2[0], g2[1]);
           }
           live_units += __any_sync(0xffffffffu, kept) ? 1u : 0u;
-          // staging box cc / 2 (64 columns), this lane's 128-byte row, 128B swizzle
-          uint8_t* rowp = stg + (cc >> 1) * 4096 + lane * 128;
+          // staging box cc / 2 (64 columns; with one box: the same again), this
+          // lane's 128-byte row, 128B swizzle
+          uint8_t* rowp = stg + (PICK ? 0 : (cc >> 1) * 4096) + lane * 128;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const int chunk = ((cc & 1) * 4 + q) ^ sw;
             *reinterpret_cast<uint4*>(rowp + chunk * 16) =
                 make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
+          }
+          if (PICK && cc == 1) {  // the first half leaves its box to the second
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(&mp.gSt, stg, gcol, grow);
+              bulk_commit_group();
+              bulk_wait_group_read0();
+            }
+            __syncwarp();
           }
         }
         // every column this warp needs is read from TMEM
@@ -621,8 +638,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SP_THREADS, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          tma_store_2d(&mp.gSt, stg, gcol, grow);
-          tma_store_2d(&mp.gSt, stg + 4096, gcol + 64, grow);
+          if (!PICK) tma_store_2d(&mp.gSt, stg, gcol, grow);
+          tma_store_2d(&mp.gSt, stg + SP_STAGING_PER_WARP - 4096, gcol + 64, grow);
           bulk_commit_group();
           // this G tile holds a kept entry: B and C tasks must read it
           if (a.nz && live_units)
@@ -688,27 +705,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SP_THREADS, 1)
         // (stored as zeros by a dC task that writes, skipped by one that adds)
         const bool empty_task = tmask == 0ull;
         if (PICK && isB && a.dC_bf16) {
-          // the finished dC tile rounded once to bf16, in two boxes of 64 columns
+          // the finished dC tile rounded once to bf16, 64 columns at a time
 #pragma unroll 1
           for (int cc = 0; cc < 4; ++cc) {
             const int c = hsel * 4 + cc;
             if (c * 32 >= nd) break;
             float v[32];
             tmem_ld32(tacc + (uint32_t)(c * 32), v);
-            uint8_t* rowp = stg + (cc >> 1) * 4096 + lane * 128;
+            uint8_t* rowp = stg + lane * 128;
 #pragma unroll
             for (int q = 0; q < 4; ++q)
               *reinterpret_cast<uint4*>(rowp + ((((cc & 1) * 4 + q) ^ (lane & 7)) << 4)) =
                   make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
                              pack_bf16x2(v[8 * q + 4], v[8 * q + 5]), pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          const int x0 = t.b * 256 + hsel * 128;
-          if (lane == 0 && row0 < a.V && hsel * 128 < nd) {
-            if (x0 < a.D) tma_store_2d(&mp.dC, stg, x0, row0);
-            if (x0 + 64 < a.D) tma_store_2d(&mp.dC, stg + 4096, x0 + 64, row0);
-            bulk_commit_group();
+            if (cc & 1) {
+              fence_proxy_async_smem();
+              __syncwarp();
+              const int x0 = t.b * 256 + hsel * 128 + (cc >> 1) * 64;
+              if (lane == 0 && row0 < a.V && x0 < a.D) {
+                tma_store_2d(&mp.dC, stg, x0, row0);
+                bulk_commit_group();
+                bulk_wait_group_read0();
+              }
+              __syncwarp();
+            }
           }
         }
 #pragma unroll 1
@@ -729,8 +749,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SP_THREADS, 1)
             // Two staging buffers in turn: the block staged here two pieces ago
             // has been read once at most one group is still reading.  (Pieces
             // are skipped only from some c on, so the turn never breaks.)
-            uint8_t* xb = stg + (cc & 1) * 4096;
-            if (lane == 0) bulk_wait_group_read<1>();
+            // (with one buffer: once none is.)
+            uint8_t* xb = stg + (PICK ? 0 : (cc & 1) * 4096);
+            if (lane == 0) bulk_wait_group_read<PICK ? 0 : 1>();
             __syncwarp();
             stage_f32_block(xb, lane, v);
             fence_proxy_async_smem();
@@ -787,8 +808,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SP_THREADS, 1)
   if (threadIdx.x == 0 && *abort_flag) atomicOr(a.status + ST_FLAGS, SF_TIMEOUT);
 }
 
-size_t bwd_stripe_smem_bytes() {
-  return 1024 + (size_t)SP_STAGES * SP_STAGE_BYTES + (size_t)SP_EPI_WARPS * SP_STAGING_PER_WARP + 512;
+template <bool PICK>
+constexpr size_t bwd_stripe_smem_bytes() {
+  return 1024 + (size_t)kStages<PICK> * SP_STAGE_BYTES + (size_t)SP_EPI_WARPS * kStagingBytes<PICK> + 512;
 }
 
 // maps: the nine tensor maps in the order of StripeMaps; grid: an even number of CTAs.
@@ -803,7 +825,7 @@ cudaError_t launch_bwd_stripe(const CUtensorMap* maps, const StripeArgs& a, void
   mp.cM = maps[6];
   mp.dE = maps[7];
   mp.dC = maps[8];
-  const size_t smem = bwd_stripe_smem_bytes();
+  const size_t smem = a.tgt_id ? bwd_stripe_smem_bytes<true>() : bwd_stripe_smem_bytes<false>();
   auto kernel = a.tgt_id ? bwd_stripe_kernel<true> : bwd_stripe_kernel<false>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
