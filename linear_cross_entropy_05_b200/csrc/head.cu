@@ -103,6 +103,24 @@ __device__ __forceinline__ float warp_max(float x) {
   return m;
 }
 
+// Sums over the warp of eight columns at once: each exchange halves the columns
+// that a lane carries; lanes 4 j .. 4 j + 3 end with column j's.
+__device__ __forceinline__ float warp_sums(float (&v)[8], int lane) {
+#pragma unroll
+  for (int n = 4, o = 16; n >= 1; n >>= 1, o >>= 1) {
+    const bool upper = (lane & o) != 0;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float send = upper ? v[i] : v[i + n], keep = upper ? v[i + n] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+    }
+  }
+  float r = v[0];
+  r += __shfl_xor_sync(0xffffffffu, r, 2);
+  r += __shfl_xor_sync(0xffffffffu, r, 1);
+  return r;
+}
+
 __device__ __forceinline__ double row_scale(const HeadArgs& a, int n) {
   const float t = a.temperature ? a.temperature[n] : a.temperature_all;
   // (an infinite temperature keeps a scale above 0, so that a logit of -inf still weighs nothing)
@@ -298,6 +316,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(HL_THREADS, 1)
         // lane j keeps column j's maximum and sum
         float my_max = 0.f;
         unsigned my_hi = 0u, my_lo = 0u;
+        float my_tail = 0.f;
 #pragma unroll
         for (int j0 = 0; j0 < 32; j0 += 8) {
           if (j0 < n_here) {
@@ -313,17 +332,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(HL_THREADS, 1)
               x[j0 + j] = in ? z : -INFINITY;
               m[j] = warp_max(x[j0 + j]);
             }
-            // each exponential in fixed point, so that the 32 of a group are
-            // summed exactly by integer reductions: units of 2^-26 from float,
-            // of 2^-51 in two words from double
+            // double: each exponential in fixed point, units of 2^-51 in two
+            // words, so that a group's 32 are summed exactly by integer
+            // reductions.  float: the largest logit's own (1 each) are counted
+            // and the others summed apart from them, so that a log-probability
+            // near 0 keeps its relative precision; the product's rounding is
+            // put back
             if (!in_double) {
+              float e[8];
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
-                const float e = ex2_approx((x[j0 + j] - m[j]) * scale_f[row + j0 + j]);
-                const unsigned sum = __reduce_add_sync(0xffffffffu, __float2uint_rn(e * 67108864.f));
+                const float d = x[j0 + j] - m[j], f = scale_f[row + j0 + j];
+                const float t = d * f;
+                const float p = ex2_approx(t);
+                // (t is not above -150, nor a number, where d is -inf)
+                e[j] = d < 0.f && t > -150.f ? fmaf(p, fmaf(d, f, -t) * LN2, p) : 0.f;
+                const unsigned ones = __popc(__ballot_sync(0xffffffffu, d == 0.f));
                 my_max = lane == j0 + j ? m[j] : my_max;
-                my_hi = lane == j0 + j ? sum : my_hi;
+                my_hi = lane == j0 + j ? ones : my_hi;
               }
+              const float tail = __shfl_sync(0xffffffffu, warp_sums(e, lane), (lane & 7) * 4);
+              my_tail = (lane >> 3) == (j0 >> 3) ? tail : my_tail;
             } else {
               // (m widened by the lane of its column; terms below 2^-80 of the
               // largest round to nothing)
@@ -351,7 +380,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(HL_THREADS, 1)
           // this warp's own sum over the tiles
           const int i = ((warp - 2) * HL_CHUNKS + c / (HL_EPI_WARPS / 4)) * 32 + lane;
           const float old = bin_max[i], top = fmaxf(old, my_max);
-          double mass = (double)my_hi * (1.0 / 67108864.0);
+          double mass = (double)my_hi + (double)my_tail;
           if (in_double) {
             mass = ((double)my_hi * 67108864.0 + (double)my_lo) * (1.0 / 2251799813685248.0);
             a.gmass[at] = mass;

@@ -16,14 +16,17 @@ pytestmark = pytest.mark.gpu
 U32 = 2.0 ** -24
 
 # Rows whose token does not hang on it get their log-sum-exp from float
-# exponentials 2^t, t <= 0, within each group (summed in double from there), of
-# which the error of log S, S = sum 2^t, is at most
-#   2^-22      ex2's own relative error
-#   30 U32     t is a difference times a factor, each rounded: 2 U32 |t| ln 2
-#              of 2^t, and sum |t| ln 2 2^t / S <= ln V + 1 < 15
-#   2^-22      the 32 terms of a group are rounded to 2^-26 of its largest
-#              (which S holds): 32 * 2^-27
-FLOAT_SUMS = 2.0 ** -21 + 30 * U32
+# exponentials 2^t, t <= 0, within each group of 32 (summed in double from
+# there); the largest logit's own is exact and kept apart.  Of the others' sum
+# the relative error is at most
+#   2^-22      ex2's own
+#   45 U32     t = (z - top) c: the difference and c are rounded, and what is put
+#              back of the product's rounding is: 3 U32 |t| ln 2 of 2^t, and
+#              sum |t| ln 2 2^t / sum 2^t <= ln V + 1 < 15
+#   6 U32      the others of a group are summed in six additions
+# and S = 1 + others (where 1 is the largest), so log S is off by at most
+# FLOAT_SUMS * others / S <= FLOAT_SUMS * log S.
+FLOAT_SUMS = 2.0 ** -22 + 51 * U32
 
 
 def make(seed, N, D, V, spread=2.0, coarse=False):
@@ -48,7 +51,7 @@ def check_top(got, z, k):
         assert np.array_equal(values[i], z[i][order].astype(np.float32))
     top = z.max(axis=1)
     want = top + np.log(np.exp(z - top[:, None]).sum(axis=1))
-    assert (np.abs(lse - want) <= FLOAT_SUMS + U32 * np.abs(want)).all()
+    assert (np.abs(lse - want) <= FLOAT_SUMS * (want - top) + 1.01 * U32 * np.abs(want) + 1e-12).all()
 
 
 @pytest.mark.parametrize("N,D,V,k", [
@@ -96,8 +99,8 @@ def check_draw(got, z, u, settings):
         k = s.get("top_k", 0)
         exact = (s.get("temperature", 1.0) > 0 and not 0 < k < z.shape[1] and
                  (s.get("top_p", 1.0) < 1 or s.get("min_p", 0.0) == 0))
-        # double sums: one rounding of the result
-        assert abs(logp[i] - lp) <= 1.01 * U32 * abs(lp) + (1e-9 if exact else FLOAT_SUMS), (i, s)
+        # double sums: one rounding of the result; else log S <= -lp is off too
+        assert abs(logp[i] - lp) <= (1.01 * U32 + (0 if exact else FLOAT_SUMS)) * abs(lp) + 1e-12, (i, s)
 
 
 @pytest.mark.parametrize("N,D,V", [(1, 8, 1), (2, 64, 31), (40, 264, 257), (33, 128, 3000), (21, 96, 20000),
@@ -138,6 +141,18 @@ def test_wide_prefixes_and_rows_full_of_ties(coarse, V, spread):
               dict(top_k=7001, top_p=0.95, min_p=0.1, temperature=1.25), dict(top_k=50), dict(), dict(temperature=0.0),
               dict(top_p=0.01), dict(top_p=1.0 - 2.0 ** -24), dict(top_p=0.6, temperature=50.0), dict(top_k=4097),
               dict(top_k=V - 1, top_p=0.99), dict(top_p=0.97, temperature=3.0, min_p=1e-5)):
+        check_draw(L.sample(E.cuda(), C.cuda(), u.cuda(), **s), z, u, s)
+
+
+def test_a_log_probability_near_zero_keeps_its_relative_precision():
+    import torch
+    import linear_cross_entropy_05_b200 as L
+    E, C, z, u = make(13, 9, 128, 30000, spread=1.5)
+    up = torch.tensor([6.0, 8.0, 10.0, 12.0, 14.0, 16.0, 18.0, 20.0, 22.0])
+    for i in range(9):   # one id stands out
+        E[i] = (E[i].float() + up[i] * C[100 * i].float() / C[100 * i].float().square().sum()).mul(32).round().div(32)
+    z = E.double().numpy() @ C.double().numpy().T
+    for s in (dict(temperature=0.0), dict(top_k=3), dict(top_p=0.9), dict(), dict(min_p=0.5)):
         check_draw(L.sample(E.cuda(), C.cuda(), u.cuda(), **s), z, u, s)
 
 
