@@ -200,6 +200,21 @@ bool make_map(CUtensorMap* map, const void* base, int64_t rows, int64_t D, int b
   return r == CUDA_SUCCESS;
 }
 
+// bf16 [rows][D], D a multiple of 64, as [D / 64][rows][64] in boxes of two
+// 64-column groups of 64 rows (16 KB, one group behind the other).
+bool make_map_groups(CUtensorMap* map, const void* base, int64_t rows, int64_t D) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc || D % BK != 0) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)BK, (cuuint64_t)rows, (cuuint64_t)(D / BK)};
+  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)BK * 2};
+  cuuint32_t box[3] = {(cuuint32_t)BK, 64, 2};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 // fp32 gradient tensor [rows][D] as 32 x 32 boxes with 128-byte swizzle: the
 // target of the backward kernel's bulk reduce-adds.
 bool make_map_f32(CUtensorMap* map, const void* base, int64_t rows, int64_t D) {
@@ -685,7 +700,7 @@ cce_status_t backward_stripes(const void* E, const void* C, void* dE, void* dC, 
                               float temperature = 1.f, bool dC_bf16 = false) {
   const StripeLayout& L = bp.stripes;
   void* G = ws + L.off_G;
-  CUtensorMap maps[9];
+  CUtensorMap maps[12];
   const int64_t Grows = (int64_t)L.p.nbuf * L.Ns_pad;
   if (!make_map(&maps[0], E, a.N, a.D, 128) || !make_map(&maps[1], C, a.V, a.D, 128) ||
       !make_map(&maps[2], G, Grows, L.Vs, 32) || !make_map(&maps[3], G, Grows, L.Vs, 128) ||
@@ -693,6 +708,12 @@ cce_status_t backward_stripes(const void* E, const void* C, void* dE, void* dC, 
       !make_map(&maps[6], C, a.V, a.D, 64) || !make_map_f32(&maps[7], dE, a.N, a.D) ||
       !(dC_bf16 ? make_map(&maps[8], dC, a.V, a.D, 32) : make_map_f32(&maps[8], dC, a.V, a.D)))
     return CCE_ERR_CUDA;
+  // (where D is not a multiple of 64 the last group would reach past the rows' ends)
+  const bool wide_boxes = tg && a.D % BK == 0;
+  if (tg && (!make_map_groups(&maps[9], G, Grows, L.Vs) ||
+             (wide_boxes && (!make_map_groups(&maps[10], E, a.N, a.D) || !make_map_groups(&maps[11], C, a.V, a.D)))))
+    return CCE_ERR_CUDA;
+  if (tg && !wide_boxes) maps[10] = maps[11] = maps[9];
   unsigned char* ctr = reinterpret_cast<unsigned char*>(ws + L.off_ctr);
   StripeArgs sa{};
   sa.N = a.N;
@@ -722,6 +743,7 @@ cce_status_t backward_stripes(const void* E, const void* C, void* dE, void* dC, 
     sa.dloss_stride = tg->dloss_stride;
     sa.dloss_scale = tg->dloss_scale;
     sa.dC_bf16 = dC_bf16 ? 1 : 0;
+    sa.wide_boxes = wide_boxes ? 1 : 0;
   }
   sa.ordered = ordered ? 1 : 0;
   sa.status = a.status;

@@ -84,6 +84,9 @@ struct StripeMaps {
   CUtensorMap cM;    // C   bf16               box {64, 64}:  C tasks, d-contiguous (MN-major)
   CUtensorMap dE;    // dE  fp32 [N][D]        box {32, 32}: reduce-add
   CUtensorMap dC;    // dC  fp32 [V][D]        box {32, 32}: store / reduce-add
+  // distillation: the MN-major operands as [columns / 64][rows][64] in boxes of
+  // {64, 64, 2}: 128 columns by one instruction
+  CUtensorMap gM2, eM2, cM2;
 };
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
@@ -167,6 +170,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SP_THREADS, 1)
     tma_prefetch_map(&mp.cM);
     tma_prefetch_map(&mp.dE);
     tma_prefetch_map(&mp.dC);
+    if constexpr (PICK) {
+      tma_prefetch_map(&mp.gM2);
+      tma_prefetch_map(&mp.eM2);
+      tma_prefetch_map(&mp.cM2);
+    }
   }
   tc_fence_before();
   cluster_sync();
@@ -393,11 +401,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SP_THREADS, 1)
               // Y = E[64 tokens][this CTA's 128 d columns]
               const int gcol = (t.a - t.s * P.vt_per_s) * BN + r * 128;
               const int grow = (t.s % P.nbuf) * a.Ns_pad + kb * BK;
-              tma_load_2d_pair(X, &mp.gM, &full[stage], gcol, grow);
-              tma_load_2d_pair(X + 8192, &mp.gM, &full[stage], gcol + 64, grow);
+              if constexpr (PICK) {
+                tma_load_3d_pair(X, &mp.gM2, &full[stage], 0, grow, gcol / 64);
+              } else {
+                tma_load_2d_pair(X, &mp.gM, &full[stage], gcol, grow);
+                tma_load_2d_pair(X + 8192, &mp.gM, &full[stage], gcol + 64, grow);
+              }
               const int d0 = t.b * 256 + r * (nd / 2);
-              tma_load_2d_pair(Y, &mp.eM, &full[stage], d0, a.tok0 + kb * BK);
-              if (half_boxes == 2) tma_load_2d_pair(Y + 8192, &mp.eM, &full[stage], d0 + 64, a.tok0 + kb * BK);
+              if (PICK && a.wide_boxes && half_boxes == 2) {
+                tma_load_3d_pair(Y, &mp.eM2, &full[stage], 0, a.tok0 + kb * BK, d0 / 64);
+              } else {
+                tma_load_2d_pair(Y, &mp.eM, &full[stage], d0, a.tok0 + kb * BK);
+                if (half_boxes == 2) tma_load_2d_pair(Y + 8192, &mp.eM, &full[stage], d0 + 64, a.tok0 + kb * BK);
+              }
             } else {
               // X = G[this CTA's 128 token rows][64 stripe columns],
               // Y = C[64 stripe rows][this CTA's 128 d columns]
@@ -405,8 +421,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SP_THREADS, 1)
                                (t.s % P.nbuf) * a.Ns_pad + t.a * 256 + r * 128);
               const int v0 = t.s * P.vt_per_s * BN + kb * BK;
               const int d0 = t.b * 256 + r * (nd / 2);
-              tma_load_2d_pair(Y, &mp.cM, &full[stage], d0, v0);
-              if (half_boxes == 2) tma_load_2d_pair(Y + 8192, &mp.cM, &full[stage], d0 + 64, v0);
+              if (PICK && a.wide_boxes && half_boxes == 2) {
+                tma_load_3d_pair(Y, &mp.cM2, &full[stage], 0, v0, d0 / 64);
+              } else {
+                tma_load_2d_pair(Y, &mp.cM, &full[stage], d0, v0);
+                if (half_boxes == 2) tma_load_2d_pair(Y + 8192, &mp.cM, &full[stage], d0 + 64, v0);
+              }
             }
             armed |= 1u << stage;
           }
@@ -813,7 +833,7 @@ constexpr size_t bwd_stripe_smem_bytes() {
   return 1024 + (size_t)kStages<PICK> * SP_STAGE_BYTES + (size_t)SP_EPI_WARPS * kStagingBytes<PICK> + 512;
 }
 
-// maps: the nine tensor maps in the order of StripeMaps; grid: an even number of CTAs.
+// maps: the tensor maps in the order of StripeMaps (the last three with targets only); grid: an even number of CTAs.
 cudaError_t launch_bwd_stripe(const CUtensorMap* maps, const StripeArgs& a, void* G, int grid, cudaStream_t stream) {
   StripeMaps mp;
   mp.eA = maps[0];
@@ -825,6 +845,9 @@ cudaError_t launch_bwd_stripe(const CUtensorMap* maps, const StripeArgs& a, void
   mp.cM = maps[6];
   mp.dE = maps[7];
   mp.dC = maps[8];
+  mp.gM2 = maps[a.tgt_id ? 9 : 4];
+  mp.eM2 = maps[a.tgt_id ? 10 : 5];
+  mp.cM2 = maps[a.tgt_id ? 11 : 6];
   const size_t smem = a.tgt_id ? bwd_stripe_smem_bytes<true>() : bwd_stripe_smem_bytes<false>();
   auto kernel = a.tgt_id ? bwd_stripe_kernel<true> : bwd_stripe_kernel<false>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);

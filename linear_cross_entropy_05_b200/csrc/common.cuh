@@ -445,6 +445,7 @@ struct StripeArgs {
   float temperature;     // G = dloss * temperature * (softmax - targets)
   int dloss_stride;      // 1, or 0: one dloss for all rows
   const float* dloss_scale;  // optional: a factor of every dloss
+  int wide_boxes;        // 1: E and C in 128-column boxes too (D a multiple of 64)
   int dC_bf16;           // 1: dC-tile tasks store bf16 (dC_add = 0; the dC map is of bf16 boxes)
 };
 
