@@ -378,6 +378,72 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SP_THREADS, 1)
         const int nd = t.type == TASK_A ? 256 : chunk_width(a.D, t.b);
         const int half_boxes = nd / 128;                 // 2, or 1 for a 128-wide chunk
         const uint32_t cta_bytes = 16384u + (t.type == TASK_A ? 16384u : 8192u * (uint32_t)half_boxes);
+        if constexpr (PICK) {
+          // Every K slice is live.  The coordinates are formed once a task and
+          // each kind has a loop of its own: this thread's time per slice is
+          // what the operand stream waits for.
+          const int ahead = nk > SP_STAGES ? nk - SP_STAGES : 0;
+          auto stream = [&](auto load) -> bool {
+            for (int j = 0; j < nk; ++j) {
+              if (leader && j == ahead) look_ahead();
+              if (!mbar_wait(&empty[stage], phase ^ 1u, wc)) return false;
+              uint8_t* X = stages + stage * SP_STAGE_BYTES;
+              if (leader) mbar_arrive_expect_tx(&full[stage], 2u * cta_bytes);
+              if (!a.withhold_loads) {
+                load(X, X + 16384, &full[stage], j * BK);
+                armed |= 1u << stage;
+              }
+              if (++stage == SP_STAGES) {
+                stage = 0;
+                phase ^= 1u;
+              }
+            }
+            return true;
+          };
+          const int g0 = (t.s % P.nbuf) * a.Ns_pad;  // first row of the stripe's buffer
+          const int d0 = t.b * 256 + r * (nd / 2);
+          bool ok;
+          if (t.type == TASK_A) {
+            // X = E[token rows of this CTA][64 d], Y = C[vocabulary rows of this CTA][64 d]
+            const int ye = a.tok0 + t.a * 256 + r * 128, yc = t.b * BN + r * 128;
+            ok = stream([&](uint8_t* X, uint8_t* Y, uint64_t* bar, int k) {
+              tma_load_2d_pair(X, &mp.eA, bar, k, ye);
+              tma_load_2d_pair(Y, &mp.cA, bar, k, yc);
+            });
+          } else if (t.type == TASK_B) {
+            // X = G[64 tokens][this CTA's 128 vocabulary columns], Y = E[64 tokens][this CTA's d columns]
+            const int gz = ((t.a - t.s * P.vt_per_s) * BN + r * 128) / 64;
+            if (a.wide_boxes && half_boxes == 2) {
+              ok = stream([&](uint8_t* X, uint8_t* Y, uint64_t* bar, int k) {
+                tma_load_3d_pair(X, &mp.gM2, bar, 0, g0 + k, gz);
+                tma_load_3d_pair(Y, &mp.eM2, bar, 0, a.tok0 + k, d0 / 64);
+              });
+            } else {
+              ok = stream([&](uint8_t* X, uint8_t* Y, uint64_t* bar, int k) {
+                tma_load_3d_pair(X, &mp.gM2, bar, 0, g0 + k, gz);
+                tma_load_2d_pair(Y, &mp.eM, bar, d0, a.tok0 + k);
+                if (half_boxes == 2) tma_load_2d_pair(Y + 8192, &mp.eM, bar, d0 + 64, a.tok0 + k);
+              });
+            }
+          } else {
+            // X = G[this CTA's 128 token rows][64 stripe columns], Y = C[64 stripe rows][this CTA's d columns]
+            const int yg = g0 + t.a * 256 + r * 128, v0 = t.s * P.vt_per_s * BN;
+            if (a.wide_boxes && half_boxes == 2) {
+              ok = stream([&](uint8_t* X, uint8_t* Y, uint64_t* bar, int k) {
+                tma_load_2d_pair(X, &mp.gK, bar, k, yg);
+                tma_load_3d_pair(Y, &mp.cM2, bar, 0, v0 + k, d0 / 64);
+              });
+            } else {
+              ok = stream([&](uint8_t* X, uint8_t* Y, uint64_t* bar, int k) {
+                tma_load_2d_pair(X, &mp.gK, bar, k, yg);
+                tma_load_2d_pair(Y, &mp.cM, bar, d0, v0 + k);
+                if (half_boxes == 2) tma_load_2d_pair(Y + 8192, &mp.cM, bar, d0 + 64, v0 + k);
+              });
+            }
+          }
+          if (!ok) goto producer_done;
+          continue;
+        }
         unsigned long long rest = tmask;  // B / C: live K blocks not yet streamed
         int blk = -1;
         for (int j = 0; j < nk; ++j) {
@@ -401,19 +467,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SP_THREADS, 1)
               // Y = E[64 tokens][this CTA's 128 d columns]
               const int gcol = (t.a - t.s * P.vt_per_s) * BN + r * 128;
               const int grow = (t.s % P.nbuf) * a.Ns_pad + kb * BK;
-              if constexpr (PICK) {
-                tma_load_3d_pair(X, &mp.gM2, &full[stage], 0, grow, gcol / 64);
-              } else {
-                tma_load_2d_pair(X, &mp.gM, &full[stage], gcol, grow);
-                tma_load_2d_pair(X + 8192, &mp.gM, &full[stage], gcol + 64, grow);
-              }
+              tma_load_2d_pair(X, &mp.gM, &full[stage], gcol, grow);
+              tma_load_2d_pair(X + 8192, &mp.gM, &full[stage], gcol + 64, grow);
               const int d0 = t.b * 256 + r * (nd / 2);
-              if (PICK && a.wide_boxes && half_boxes == 2) {
-                tma_load_3d_pair(Y, &mp.eM2, &full[stage], 0, a.tok0 + kb * BK, d0 / 64);
-              } else {
-                tma_load_2d_pair(Y, &mp.eM, &full[stage], d0, a.tok0 + kb * BK);
-                if (half_boxes == 2) tma_load_2d_pair(Y + 8192, &mp.eM, &full[stage], d0 + 64, a.tok0 + kb * BK);
-              }
+              tma_load_2d_pair(Y, &mp.eM, &full[stage], d0, a.tok0 + kb * BK);
+              if (half_boxes == 2) tma_load_2d_pair(Y + 8192, &mp.eM, &full[stage], d0 + 64, a.tok0 + kb * BK);
             } else {
               // X = G[this CTA's 128 token rows][64 stripe columns],
               // Y = C[64 stripe rows][this CTA's 128 d columns]
@@ -421,12 +479,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SP_THREADS, 1)
                                (t.s % P.nbuf) * a.Ns_pad + t.a * 256 + r * 128);
               const int v0 = t.s * P.vt_per_s * BN + kb * BK;
               const int d0 = t.b * 256 + r * (nd / 2);
-              if (PICK && a.wide_boxes && half_boxes == 2) {
-                tma_load_3d_pair(Y, &mp.cM2, &full[stage], 0, v0, d0 / 64);
-              } else {
-                tma_load_2d_pair(Y, &mp.cM, &full[stage], d0, v0);
-                if (half_boxes == 2) tma_load_2d_pair(Y + 8192, &mp.cM, &full[stage], d0 + 64, v0);
-              }
+              tma_load_2d_pair(Y, &mp.cM, &full[stage], d0, v0);
+              if (half_boxes == 2) tma_load_2d_pair(Y + 8192, &mp.cM, &full[stage], d0 + 64, v0);
             }
             armed |= 1u << stage;
           }
