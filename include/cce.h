@@ -331,7 +331,9 @@ CCE_API cce_status_t cce_backward_shard(const void* E, const void* C_shard, cons
  * and no gradient.  An id that is listed twice counts twice.  A live entry
  * with an id outside [0, V) or a NaN or +inf logit makes the row's loss NaN,
  * sets status flag bit 1, and the row has no gradient.  The entries need no
- * order.  1 <= K <= 1024; temperature finite and > 0.
+ * order.  1 <= K <= 1024; 1e-3 <= temperature <= 1e6 (the softmax of the
+ * backward is formed from lse in fp32: its relative error is about
+ * |lse| 2^-24).
  * The N x V logits are not written to memory: the listed logits are taken
  * from the tiles of the log-sum-exp pass.  ids is int64, teacher float or
  * bf16 (cce_dtype_t). */
@@ -340,7 +342,8 @@ typedef enum { CCE_DTYPE_F32 = 0, CCE_DTYPE_BF16 = 1 } cce_dtype_t;
 /* Workspace bytes of cce_distill_forward / cce_distill_backward (0 if the
  * sizes or flags are invalid; the forward's also without a usable device):
  * the forward's partials (12 bytes per token and vocabulary split) and
- * 8 K + 8 bytes per token; the backward's stripes as for CCE_BWD_STRIPES,
+ * 8 K + 8 bytes per token; the backward's stripes of G (24 KB per token of at
+ * most 16384 and, for few tokens, as many stripes as 128 MB holds), a copy of E,
  * 8 K + 8 bytes per token and, with CCE_BWD_BF16_GRADS, the fp32 sums of dE
  * (and of dC if it is accumulated into or N > 16384). */
 CCE_API size_t cce_distill_forward_workspace_size(int64_t N, int64_t D, int64_t V, int64_t K);
@@ -362,7 +365,8 @@ CCE_API cce_status_t cce_distill_forward(const void* E, const void* C, const int
  * null: with inv_count there, the gradient of dloss[0] times the mean),
  *     G[i,v] = dloss[i] T (exp(z_iv / T - lse[i]) - sum_{k: ids[i,k] = v} p[i,k]),
  *     dE = G C,  dC = G^T E,
- * through stripes of G as with CCE_BWD_STRIPES (no entry is filtered).  lse is
+ * through stripes of G as with CCE_BWD_STRIPES (no entry is filtered).  What
+ * E, lse and dloss hold for a row without a gradient is not looked at.  lse is
  * cce_distill_forward's on the same inputs and temperature.  flags:
  * CCE_BWD_DETERMINISTIC (dE summed in stripe order), CCE_BWD_BF16_GRADS,
  * CCE_BWD_ACCUMULATE, with their meaning in cce_backward_ex. */
@@ -424,8 +428,9 @@ CCE_API cce_status_t cce_sample(const void* E, const void* C, int64_t N, int64_t
                                 void* workspace, size_t workspace_bytes, void* stream);
 
 /* Synchronises `stream`, then copies the status block of `workspace` (as left
- * by the last call that used it) into *out.  Returns CCE_ERR_TIMEOUT or
- * CCE_ERR_BAD_LABEL if the corresponding flag is set, else CCE_OK. */
+ * by the last call that used it) into *out.  Returns CCE_ERR_TIMEOUT,
+ * CCE_ERR_BAD_LABEL or CCE_ERR_NONFINITE if the corresponding flag is set,
+ * else CCE_OK. */
 CCE_API cce_status_t cce_read_status(const void* workspace, void* stream, cce_counters_t* out);
 
 /* Human-readable name of a status code (static storage). */

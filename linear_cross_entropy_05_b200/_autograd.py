@@ -52,6 +52,7 @@ class LinearDistillation(torch.autograd.Function):
         return mean
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, g):
         E, C, ids, teacher, lse, inv_count = ctx.saved_tensors
         dE, dC = _distill_backward(E, C, ids, teacher, lse, g.to(torch.float32), ctx.temperature, ctx.ignore_index,

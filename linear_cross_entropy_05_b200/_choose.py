@@ -60,7 +60,7 @@ def sample(E, C, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, workspace: O
             check_tensor(value, name, (N,), dtype, E.device)
             setattr(settings, name, value.data_ptr())
         else:
-            setattr(settings, name + "_all", min(int(value), 2 ** 31 - 1) if name == "top_k" else float(value))
+            setattr(settings, name + "_all", min(max(int(value), -1), 2 ** 31 - 1) if name == "top_k" else float(value))
     with Launch(E.device, stream, workspace) as run:
         if out is None:
             token, logp = run.empty((N,), torch.int64), run.empty((N,), torch.float32)

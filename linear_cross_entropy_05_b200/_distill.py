@@ -102,7 +102,8 @@ def distill_forward(E, C, ids, teacher, temperature: float = 1.0, ignore_index: 
     With p the softmax of a row's teacher logits over its entries at
     `temperature` T and q the student's softmax of E C^T / T over all of the
     vocabulary, loss = T^2 sum_k p_k log(p_k / q_{ids_k}).  lse is the
-    log-sum-exp of the logits divided by T, which distill_backward needs.
+    log-sum-exp of the logits divided by T, which distill_backward needs.  T is
+    from 1e-3 to 1e6.
     mean: optionally two fp32 scalar tensors that receive the mean loss over
     the rows with an entry and one over their number."""
     N, D, V = check_head(E, C)
@@ -133,11 +134,13 @@ def distill_backward(E, C, ids, teacher, lse, dloss, temperature: float = 1.0, i
     distill_forward (every entry of the softmax's gradient; no filter): fp32,
     or bf16 with bf16_grads.  dloss is [N], or a scalar tensor for all rows;
     dloss_scale, a scalar tensor, multiplies it (with distill_forward's second
-    mean: the gradient of dloss times the mean).  deterministic=True sums dE in a fixed order;
-    accumulate=True adds to the tensors given in `out` (required).  The
-    logits are formed again on chip; the scratch is about 24 KB per token (at
-    most ~400 MB), plus the fp32 sums of dE for bf16 outputs (and of dC with
-    accumulate or more than 16384 tokens)."""
+    mean: the gradient of dloss times the mean).  deterministic=True sums dE in
+    a fixed order; accumulate=True adds to the tensors given in `out`
+    (required).  The
+    logits are formed again on chip; the scratch is 24 KB per token (of at most
+    16384) or, for few tokens, up to 128 MB, a copy of E, and the fp32 sums of
+    dE for bf16 outputs (and of dC with accumulate or more than 16384 tokens).
+    What E, lse and dloss hold for a row without entries is not looked at."""
     N, D, V = check_head(E, C)
     K, dtype = _check_targets(ids, teacher, N, E.device)
     check_tensor(lse, "lse", (N,), torch.float32, E.device)
@@ -159,6 +162,7 @@ def distill_backward(E, C, ids, teacher, lse, dloss, temperature: float = 1.0, i
         ws = run.scratch(cce_distill_backward_workspace_size(N, D, V, K, flags), "cce_distill_backward_workspace_size")
         cce_distill_backward(E.data_ptr(), C.data_ptr(), ids.data_ptr(), teacher.data_ptr(), dtype, lse.data_ptr(),
                              dloss.data_ptr(), 1 if dloss.dim() else 0,
-                             0 if dloss_scale is None else dloss_scale.data_ptr(), N, D, V, K, ignore_index, float(temperature), flags, dE.data_ptr(),
-                             dC.data_ptr(), ws.data_ptr(), ws.numel(), run.ptr)
+                             0 if dloss_scale is None else dloss_scale.data_ptr(), N, D, V, K, ignore_index,
+                             float(temperature), flags, dE.data_ptr(), dC.data_ptr(), ws.data_ptr(), ws.numel(),
+                             run.ptr)
     return dE, dC

@@ -325,7 +325,7 @@ struct StripeLayout {
 // 48 us; 21 us in all with stripes of 256); and as many buffers as kStripeRoom
 // holds, so that a few tokens' stripes, whose tasks do not fill the GPU, do not
 // wait for one another (6 tokens x 744 x 180434: 802 us with three buffers,
-// WIDE us with all 45).
+// 460 us with all 45).
 constexpr size_t kStripeRoom = size_t(128) << 20;
 StripeLayout plan_stripes(int64_t N, int64_t D, int64_t V, size_t base, int narrow_pairs = 0) {
   StripeLayout L{};
@@ -1070,10 +1070,11 @@ bool distill_sizes_ok(int64_t N, int64_t D, int64_t V, int64_t K) {
 }
 
 // Workspace: status | forward: partials, split sums | row kinds | entropies |
-// sorted ids | weights | backward: fp32 sums of bf16 outputs, stripes.
+// sorted ids | weights | backward: E without dead rows, fp32 sums of bf16
+// outputs, stripes.
 struct DistillLayout {
   FwdPlan fwd;        // forward only
-  size_t off_dot, off_kind, off_ent, off_id, off_w, off_dE32, off_dC32, bytes;
+  size_t off_dot, off_kind, off_ent, off_id, off_w, off_E, off_dE32, off_dC32, bytes;
   bool dC_direct;     // backward, bf16 outputs: the dC tiles are stored as bf16 by the stripe kernel
   StripeLayout stripes;
 };
@@ -1099,6 +1100,8 @@ constexpr unsigned kDistillFlags = CCE_BWD_DETERMINISTIC | CCE_BWD_BF16_GRADS | 
 bool plan_distill_backward(int64_t N, int64_t D, int64_t V, int64_t K, unsigned flags, DistillLayout* L) {
   if (!distill_sizes_ok(N, D, V, K) || (flags & ~kDistillFlags)) return false;
   plan_targets(N, K, STATUS_BYTES, L);
+  L->off_E = L->bytes;
+  L->bytes += align_up((size_t)N * D * 2, 256);
   const bool bf16 = (flags & CCE_BWD_BF16_GRADS) != 0;
   // One launch covers every token and nothing is added to: each dC tile is
   // final when its task ends, and is rounded and stored there (no fp32 copy
@@ -1119,11 +1122,13 @@ bool plan_distill_backward(int64_t N, int64_t D, int64_t V, int64_t K, unsigned 
   return true;
 }
 
-bool temperature_ok(float t) { return t > 0.f && t <= 3.0e38f && 1.f / t > 0.f && LOG2E / t <= 3.0e38f; }
+// The gradient's softmax is formed from lse in fp32, so its relative error is
+// about |lse| 2^-24; logits of 100 at T = 1e-3 still leave it at 0.6 %.
+bool temperature_ok(float t) { return t >= 1e-3f && t <= 1e6f; }
 
 cce_status_t prepare_targets(const int64_t* ids, const void* teacher, int teacher_dtype, int64_t N, int64_t V,
                              int64_t K, int64_t ignore_index, float temperature, char* ws, const DistillLayout& L,
-                             TargetBuffers* tg, cudaStream_t stream) {
+                             TargetBuffers* tg, cudaStream_t stream, const void* E = nullptr, int64_t D = 0) {
   tg->id = reinterpret_cast<int*>(ws + L.off_id);
   tg->w = reinterpret_cast<float*>(ws + L.off_w);
   tg->neg_entropy = reinterpret_cast<float*>(ws + L.off_ent);
@@ -1142,6 +1147,9 @@ cce_status_t prepare_targets(const int64_t* ids, const void* teacher, int teache
   t.tgt_w = tg->w;
   t.neg_entropy = tg->neg_entropy;
   t.row_kind = tg->row_kind;
+  t.D = (int)D;
+  t.E = E;
+  t.E_live = E ? ws + L.off_E : nullptr;
   t.status = reinterpret_cast<unsigned long long*>(ws);
   return launch_distill_targets(t, stream) == cudaSuccess ? CCE_OK : CCE_ERR_CUDA;
 }
@@ -1224,7 +1232,8 @@ cce_status_t cce_distill_backward(const void* E, const void* C, const int64_t* i
   char* ws = reinterpret_cast<char*>(workspace);
   if (cudaMemsetAsync(ws, 0, STATUS_BYTES, stream) != cudaSuccess) return CCE_ERR_CUDA;
   TargetBuffers tg{};
-  cce_status_t st = prepare_targets(ids, teacher, teacher_dtype, N, V, K, ignore_index, temperature, ws, L, &tg, stream);
+  cce_status_t st = prepare_targets(ids, teacher, teacher_dtype, N, V, K, ignore_index, temperature, ws, L, &tg, stream,
+                                    E, D);
   if (st != CCE_OK) return st;
 
   const bool bf16 = (flags & CCE_BWD_BF16_GRADS) != 0;
@@ -1250,7 +1259,7 @@ cce_status_t cce_distill_backward(const void* E, const void* C, const int64_t* i
   a.trace_cap = g_bwd_trace_cap.load();
   tg.dloss_stride = dloss_stride;
   tg.dloss_scale = dloss_scale;
-  st = backward_stripes(E, C, dE32, dC_sum, bp, a, acc32, (flags & CCE_BWD_DETERMINISTIC) != 0, di.sms, ws, stream,
+  st = backward_stripes(ws + L.off_E, C, dE32, dC_sum, bp, a, acc32, (flags & CCE_BWD_DETERMINISTIC) != 0, di.sms, ws, stream,
                         nullptr, &tg, temperature, L.dC_direct);
   if (st != CCE_OK || !bf16) return st;
   if (launch_f32_to_bf16(dE32, dE, (size_t)N * D, accumulate, di.sms, stream) != cudaSuccess) return CCE_ERR_CUDA;

@@ -111,6 +111,11 @@ struct TargetArgs {
   float* tgt_w;         // [N][K] out: the teacher's probabilities in that order
   float* neg_entropy;   // [N] out: sum_k p_k log p_k
   int* row_kind;        // [N] out: RowKind
+  // backward: E [N][D] and its copy with zeros in the rows that are not
+  // ROW_LIVE, whose NaN or inf must not reach dC = G^T E as 0 * NaN
+  int D;
+  const void* E;
+  void* E_live;
   unsigned long long* status;
 };
 struct DistillFinArgs {

@@ -12,7 +12,9 @@
 //
 // distill_targets  one block per row: p, sum p log p, and the entries sorted
 //                  by id, so that the logit and gradient tiles, which walk
-//                  the vocabulary in order, meet them one after another.
+//                  the vocabulary in order, meet them one after another.  For
+//                  the backward also the copy of E that it reads: 4 N D bytes
+//                  beside products of 6 N V D.
 // distill_finalize merges the splits' (max, sum, weighted logits) into lse
 //                  and loss; 32 rows x 8 split lanes per block, so the
 //                  [split][row] partials are read in whole lines.  The block
@@ -85,6 +87,12 @@ __global__ void __launch_bounds__(256) distill_targets_kernel(const TargetArgs a
     a.row_kind[row] = kind;
     if (bad) atomicOr(a.status + ST_FLAGS, SF_BAD_LABEL);
     if (kind != ROW_LIVE) a.neg_entropy[row] = 0.f;
+  }
+  if (a.E_live) {
+    const uint4* src = reinterpret_cast<const uint4*>(a.E) + (size_t)row * (a.D / 8);
+    uint4* dst = reinterpret_cast<uint4*>(a.E_live) + (size_t)row * (a.D / 8);
+#pragma unroll 4
+    for (int i = tid; i < a.D / 8; i += blockDim.x) dst[i] = kind == ROW_LIVE ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
   }
   if (kind != ROW_LIVE) {
     for (int k = tid; k < a.K; k += blockDim.x) {
@@ -204,7 +212,8 @@ __global__ void __launch_bounds__(256) distill_finalize_kernel(const DistillFinA
 cudaError_t launch_distill_targets(const TargetArgs& a, cudaStream_t stream) {
   int n_sort = 32;
   while (n_sort < a.K) n_sort <<= 1;
-  const int threads = n_sort / 2 < 32 ? 32 : (n_sort / 2 > 256 ? 256 : n_sort / 2);
+  const int least = a.E_live ? 128 : 32;
+  const int threads = n_sort / 2 < least ? least : (n_sort / 2 > 256 ? 256 : n_sort / 2);
   const size_t smem = (size_t)a.K * 8 + (size_t)n_sort * 8 + 64;
   distill_targets_kernel<<<a.N, threads, smem, stream>>>(a, n_sort);
   return cudaGetLastError();

@@ -32,7 +32,7 @@ def test_forward(L):
     assert call(a5=0) == 1 and call(a6=252) == 1 and call(a7=0) == 1
     assert call(a8=0) == 1 and call(a8=1025) == 1                     # K
     assert call(a7=(1 << 31) - 1, a6=8) == 1                          # ids of a tile's end must fit int32
-    for T in (0.0, -2.0, float("nan"), float("inf"), 1e-45):
+    for T in (0.0, -2.0, float("nan"), float("inf"), 1e-45, 0.9e-3, 1.1e6):
         assert call(a10=T) == 1
     assert call(a0=P + 8) == 2 and call(a2=P + 4) == 2 and call(a3=P + 2) == 2 and call(a15=P + 128) == 2
     assert call(a3=P + 2, a4=1) == 4                                  # bf16 logits on 2-byte addresses
@@ -63,14 +63,14 @@ def test_backward_workspace(L):
     size = L.cce_distill_backward_workspace_size
     N, D, V, K = 8192, 2304, 256000, 64
     stripes = (L.cce_backward_workspace_size_ex(N, D, V, 16) - L.cce_backward_workspace_size(N, D, V))
-    base = 256 + 2 * up(4 * N) + 2 * up(4 * N * K) + stripes
+    base = 256 + 2 * up(4 * N) + 2 * up(4 * N * K) + up(2 * N * D) + stripes
     assert size(N, D, V, K, 0) == size(N, D, V, K, 1) == size(N, D, V, K, 4) == base
     assert size(N, D, V, K, 2) == base + up(4 * N * D)                        # dC is rounded where it is formed
     assert size(N, D, V, K, 6) == base + up(4 * N * D) + up(4 * V * D)        # accumulated: fp32 sums first
     assert size(N, D, V, 0, 0) == 0 and size(N, D, V, 1025, 0) == 0 and size(N, D, V, K, 16) == 0
     # few dE tiles: narrower stripes, as many columns of buffers
     assert size(256, 256, 4096, 8, 0) == 256 + 2 * up(4 * 256) + 2 * up(4 * 256 * 8) + \
-        up(8 + 4 * (16 + 16 + 16 + 1) + 16) + up(16 * 256 * 256 * 2)
+        up(2 * 256 * 256) + up(8 + 4 * (16 + 16 + 16 + 1) + 16) + up(16 * 256 * 256 * 2)
     big = size(16385, 256, 4096, 4, 2)
     assert big >= up(4 * 16385 * 256) + up(4 * 4096 * 256)                    # several launches: fp32 sums first
     assert L.cce_distill_forward_workspace_size(N, D, V, K) == 0              # no device here

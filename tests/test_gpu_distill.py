@@ -333,3 +333,27 @@ def test_refusals():
         L.distill_backward(E, C, ids, t, dl, dl, accumulate=True)
     with pytest.raises(L.CCEError):
         L.distill_forward(E[:0], C, ids[:0], t[:0])
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+def test_rows_without_a_gradient_may_hold_anything(bf16):
+    """NaN and inf in E, lse and dloss of padded and of bad rows reach nothing."""
+    import torch
+    import linear_cross_entropy_05_b200 as L
+    N, D, V, K = 140, 136, 1000, 5
+    E, C, ids, t, dl = make(81, N, D, V, K)
+    dead = [0, 3, 64, 131, 139]
+    ids[dead] = IGN
+    ids[3, 2] = V + 5                                # bad, not empty
+    clean = [x.cuda() for x in (E, C, ids, t)]
+    want_loss, lse = L.distill_forward(*clean, temperature=2.0)
+    want = L.distill_backward(*clean, lse, dl.cuda(), temperature=2.0, deterministic=True, bf16_grads=bf16)
+    E[dead[::2]] = float("nan")
+    E[dead[1::2]] = float("inf")
+    dl[dead] = float("nan")
+    dirty = [x.cuda() for x in (E, C, ids, t)]
+    loss, lse = L.distill_forward(*dirty, temperature=2.0)
+    assert torch.equal(loss.nan_to_num(nan=-1), want_loss.nan_to_num(nan=-1))
+    got = L.distill_backward(*dirty, lse, dl.cuda(), temperature=2.0, deterministic=True, bf16_grads=bf16)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert (got[0][dead] == 0).all() and torch.isfinite(got[1].float()).all()
