@@ -420,6 +420,7 @@ struct TargetBuffers {
   float* neg_entropy;
   int* row_kind;
   int K;
+  bool sliced;               // forward
   int dloss_stride;          // backward
   const float* dloss_scale;
 };
@@ -457,6 +458,7 @@ cce_status_t launch_logit_pass(const void* E, const void* C, int64_t N, int64_t 
     a.tgt_w = tg->w;
     a.tgt_k = tg->K;
     a.dot = dot;
+    a.sliced = tg->sliced ? 1 : 0;
   }
   a.scale2 = scale2;
   a.sched = p.pair ? g_fwd_order.load() : 0;
@@ -1062,6 +1064,7 @@ cce_status_t cce_backward_shard(const void* E, const void* C_shard, const int64_
 // ---------------------------------------------------------------------------
 namespace {
 
+constexpr int64_t kWholeD = 1024;      // a larger D is summed in parts (PICK_SLICES in fwd.cu has both sides)
 constexpr int64_t kMaxTargets = 1024;  // the sort network of distill_targets in shared memory (16 KB)
 
 bool distill_sizes_ok(int64_t N, int64_t D, int64_t V, int64_t K) {
@@ -1074,6 +1077,8 @@ bool distill_sizes_ok(int64_t N, int64_t D, int64_t V, int64_t K) {
 // outputs, stripes.
 struct DistillLayout {
   FwdPlan fwd;        // forward only
+  bool sliced;        // (see PICK_SLICES)
+  int n_part;
   size_t off_dot, off_kind, off_ent, off_id, off_w, off_E, off_dE32, off_dC32, bytes;
   bool dC_direct;     // backward, bf16 outputs: the dC tiles are stored as bf16 by the stripe kernel
   StripeLayout stripes;
@@ -1089,8 +1094,10 @@ void plan_targets(int64_t N, int64_t K, size_t at, DistillLayout* L) {
 
 bool plan_distill_forward(int64_t N, int64_t D, int64_t V, int64_t K, DistillLayout* L) {
   if (!distill_sizes_ok(N, D, V, K) || !plan_forward(N, D, V, &L->fwd, true)) return false;
-  L->off_dot = L->fwd.ws_bytes;
-  plan_targets(N, K, L->off_dot + align_up((size_t)L->fwd.n_split * N * 4, 256), L);
+  L->sliced = D > kWholeD;
+  L->n_part = L->fwd.n_split * (L->sliced ? 2 : 1);
+  L->off_dot = STATUS_BYTES + align_up((size_t)L->n_part * N * sizeof(float2), 256);
+  plan_targets(N, K, L->off_dot + align_up((size_t)L->n_part * N * 4, 256), L);
   return true;
 }
 
@@ -1191,11 +1198,12 @@ cce_status_t cce_distill_forward(const void* E, const void* C, const int64_t* id
   cce_status_t st = prepare_targets(ids, teacher, teacher_dtype, N, V, K, ignore_index, temperature, ws, L, &tg, stream);
   if (st != CCE_OK) return st;
   float* dot = reinterpret_cast<float*>(ws + L.off_dot);
+  tg.sliced = L.sliced;
   st = launch_logit_pass(E, C, N, D, V, L.fwd, ws, nullptr, stream, &tg, dot, LOG2E / temperature);
   if (st != CCE_OK) return st;
   DistillFinArgs f{};
   f.N = (int)N;
-  f.n_split = L.fwd.n_split;
+  f.n_part = L.n_part;
   f.temperature = temperature;
   f.partial = reinterpret_cast<const float2*>(ws + STATUS_BYTES);
   f.dot = dot;

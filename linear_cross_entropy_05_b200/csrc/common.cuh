@@ -82,6 +82,9 @@ struct FwdArgs {
   const float* tgt_w;  // [N][tgt_k]
   int tgt_k;
   float* dot;          // [n_split][N]
+  // 1: logits are summed in parts of D, and each split leaves two partials
+  // (and two dots), for the halves of its tiles: [2 n_split][N]
+  int sliced;
   float scale2;        // log2(e) / temperature: exp(z / T) = 2^(scale2 z)
 };
 
@@ -119,10 +122,10 @@ struct TargetArgs {
   unsigned long long* status;
 };
 struct DistillFinArgs {
-  int N, n_split;
+  int N, n_part;
   float temperature;
-  const float2* partial;     // [n_split][N]
-  const float* dot;          // [n_split][N]
+  const float2* partial;     // [n_part][N]
+  const float* dot;          // [n_part][N]
   const float* neg_entropy;  // [N]
   const int* row_kind;       // [N]
   unsigned long long* status;  // (word ST_NEXT_TILE counts finished blocks)

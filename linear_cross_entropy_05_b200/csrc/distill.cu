@@ -16,7 +16,7 @@
 //                  the backward also the copy of E that it reads: 4 N D bytes
 //                  beside products of 6 N V D.
 // distill_finalize merges the splits' (max, sum, weighted logits) into lse
-//                  and loss; 32 rows x 8 split lanes per block, so the
+//                  and loss; 32 rows x 16 split lanes per block, so the
 //                  [split][row] partials are read in whole lines.  The block
 //                  that finishes last adds up the mean, in a fixed order.
 #include <cuda_bf16.h>
@@ -28,8 +28,8 @@ namespace cce {
 
 namespace {
 
-// Reduction of one double per thread over the block (at most 256 threads,
-// whole warps), in a fixed order; every thread gets the result.
+// Reduction of one double per thread over the block (whole warps; buf holds
+// one per warp), in a fixed order; every thread gets the result.
 template <bool MAX>
 __device__ __forceinline__ double block_reduce(double v, double* buf) {
 #pragma unroll
@@ -47,6 +47,8 @@ __device__ __forceinline__ double block_reduce(double v, double* buf) {
 }
 
 }  // namespace
+
+constexpr int FIN_PARTS = 16;
 
 // n_sort: K rounded up to a power of two (the sort network's size)
 __global__ void __launch_bounds__(256) distill_targets_kernel(const TargetArgs a, int n_sort) {
@@ -139,10 +141,10 @@ __global__ void __launch_bounds__(256) distill_targets_kernel(const TargetArgs a
   }
 }
 
-__global__ void __launch_bounds__(256) distill_finalize_kernel(const DistillFinArgs a) {
-  __shared__ float sm[8][32];
-  __shared__ float ss[8][32];
-  __shared__ double sd[8][32];
+__global__ void __launch_bounds__(32 * FIN_PARTS) distill_finalize_kernel(const DistillFinArgs a) {
+  __shared__ float sm[FIN_PARTS][32];
+  __shared__ float ss[FIN_PARTS][32];
+  __shared__ double sd[FIN_PARTS][32];
   __shared__ int s_last;
   const int lane = threadIdx.x, part = threadIdx.y;
   const int row = blockIdx.x * 32 + lane;
@@ -150,7 +152,7 @@ __global__ void __launch_bounds__(256) distill_finalize_kernel(const DistillFinA
   float M = -INFINITY, s = 0.f;
   double dot = 0.0;
   if (row < a.N) {
-    for (int r = part; r < a.n_split; r += 8) {
+    for (int r = part; r < a.n_part; r += FIN_PARTS) {
       const float2 p = a.partial[(size_t)r * a.N + row];
       dot += (double)a.dot[(size_t)r * a.N + row];
       const float m = fmaxf(M, p.x);
@@ -163,10 +165,10 @@ __global__ void __launch_bounds__(256) distill_finalize_kernel(const DistillFinA
   sd[part][lane] = dot;
   __syncthreads();
   if (part == 0 && row < a.N) {
-    for (int q = 1; q < 8; ++q) M = fmaxf(M, sm[q][lane]);
+    for (int q = 1; q < FIN_PARTS; ++q) M = fmaxf(M, sm[q][lane]);
     s = 0.f;
     dot = 0.0;
-    for (int q = 0; q < 8; ++q) {
+    for (int q = 0; q < FIN_PARTS; ++q) {
       if (sm[q][lane] != -INFINITY) s += ss[q][lane] * exp2f((sm[q][lane] - M) * scale2);
       dot += sd[q][lane];
     }
@@ -194,7 +196,7 @@ __global__ void __launch_bounds__(256) distill_finalize_kernel(const DistillFinA
   if (!s_last) return;
   __threadfence();
   double sum = 0.0, n = 0.0;
-  for (int i = tid; i < a.N; i += 256) {
+  for (int i = tid; i < a.N; i += 32 * FIN_PARTS) {
     if (a.row_kind[i] != ROW_EMPTY) {
       sum += (double)__ldcg(a.loss + i);
       n += 1.0;
@@ -220,7 +222,7 @@ cudaError_t launch_distill_targets(const TargetArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_distill_finalize(const DistillFinArgs& a, cudaStream_t stream) {
-  distill_finalize_kernel<<<(a.N + 31) / 32, dim3(32, 8), 0, stream>>>(a);
+  distill_finalize_kernel<<<(a.N + 31) / 32, dim3(32, FIN_PARTS), 0, stream>>>(a);
   return cudaGetLastError();
 }
 

@@ -54,10 +54,53 @@ struct RowTargets {
   __device__ __forceinline__ void load() { next = pos < n ? __ldg(ids + pos) : INT_MAX; }
 };
 
+// Fold 32 columns from cbase on into the row's running (max, sum exp).
+template <bool PICK>
+__device__ __forceinline__ void lse_fold_columns(float (&x)[32], int cbase, const FwdArgs& a, float& mrun, float& srun,
+                                                 RowTargets& tg) {
+  const float scale2 = PICK ? a.scale2 : LOG2E;
+  if constexpr (PICK) {
+    while (__any_sync(0xffffffffu, tg.next < cbase + 32)) {
+      const int at = tg.next - cbase;
+      float z = 0.f;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) z = (j == at) ? x[j] : z;
+      if (at < 32) {
+        tg.dot = fmaf(__ldg(tg.w + tg.pos), z, tg.dot);
+        ++tg.pos;
+        tg.load();
+      }
+    }
+  }
+  const int nvalid = a.V - cbase;
+  if (nvalid < 32) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (j >= nvalid) x[j] = -INFINITY;
+  }
+  float cm0 = x[0], cm1 = x[1];
+#pragma unroll
+  for (int j = 2; j < 32; j += 2) {
+    cm0 = fmaxf(cm0, x[j]);
+    cm1 = fmaxf(cm1, x[j + 1]);
+  }
+  const float mnew = fmaxf(mrun, fmaxf(cm0, cm1));
+  const float ms = mnew * scale2;
+  float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+  for (int j = 0; j < 32; j += 4) {
+    s0 += ex2_approx(fmaf(x[j], scale2, -ms));
+    s1 += ex2_approx(fmaf(x[j + 1], scale2, -ms));
+    s2 += ex2_approx(fmaf(x[j + 2], scale2, -ms));
+    s3 += ex2_approx(fmaf(x[j + 3], scale2, -ms));
+  }
+  srun = srun * ex2_approx(fmaf(mrun, scale2, -ms)) + ((s0 + s1) + (s2 + s3));
+  mrun = mnew;
+}
+
 template <bool DUMP, bool PICK>
 __device__ __forceinline__ void lse_fold_tile(uint32_t tbase, int col0, int row, const FwdArgs& a, float& mrun,
                                               float& srun, RowTargets& tg) {
-  const float scale2 = PICK ? a.scale2 : LOG2E;
 #pragma unroll 1
   for (int c = 0; c < BN / 32; ++c) {
     const int cbase = col0 + c * 32;
@@ -71,43 +114,7 @@ __device__ __forceinline__ void lse_fold_tile(uint32_t tbase, int col0, int row,
         for (int j = 0; j < 32; ++j) dst[j] = x[j];
       }
     }
-    if constexpr (PICK) {
-      while (__any_sync(0xffffffffu, tg.next < cbase + 32)) {
-        const int at = tg.next - cbase;
-        float z = 0.f;
-#pragma unroll
-        for (int j = 0; j < 32; ++j) z = (j == at) ? x[j] : z;
-        if (at < 32) {
-          tg.dot = fmaf(__ldg(tg.w + tg.pos), z, tg.dot);
-          ++tg.pos;
-          tg.load();
-        }
-      }
-    }
-    const int nvalid = a.V - cbase;
-    if (nvalid < 32) {
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (j >= nvalid) x[j] = -INFINITY;
-    }
-    float cm0 = x[0], cm1 = x[1];
-#pragma unroll
-    for (int j = 2; j < 32; j += 2) {
-      cm0 = fmaxf(cm0, x[j]);
-      cm1 = fmaxf(cm1, x[j + 1]);
-    }
-    const float mnew = fmaxf(mrun, fmaxf(cm0, cm1));
-    const float ms = mnew * scale2;
-    float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
-#pragma unroll
-    for (int j = 0; j < 32; j += 4) {
-      s0 += ex2_approx(fmaf(x[j], scale2, -ms));
-      s1 += ex2_approx(fmaf(x[j + 1], scale2, -ms));
-      s2 += ex2_approx(fmaf(x[j + 2], scale2, -ms));
-      s3 += ex2_approx(fmaf(x[j + 3], scale2, -ms));
-    }
-    srun = srun * ex2_approx(fmaf(mrun, scale2, -ms)) + ((s0 + s1) + (s2 + s3));
-    mrun = mnew;
+    lse_fold_columns<PICK>(x, cbase, a, mrun, srun, tg);
   }
 }
 
@@ -378,8 +385,27 @@ cudaError_t read_l2_halves(unsigned* out, int n) {
 // arrive on both CTAs' barriers, and both epilogues release the accumulator
 // on the leader's barrier.  No TMA multicast is used.
 // ----------------------------------------------------------------------------
-template <bool DUMP, int S, bool PICK>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
+// PICK_SLICES (long rows of E): the tensor cores round every addition into an
+// accumulator towards zero, about D / 16 times a logit, which leaves a D = 4096
+// head's largest logits, and with them the loss, 3e-6 short (relatively; 5e-6
+// at 8192).  A divergence may itself be small beside the log-sum-exp it is
+// formed from, so here the accumulator is handed over every kSliceSteps * 64 of
+// D, and the parts are added in registers, rounded to nearest: eight epilogue
+// warps, two per lane group, hold 128 columns each while the next part is being
+// formed.  Loss error and time, whole -> in parts of 1024:
+//   1000 x 2048 x 128256   1.4e-6 -> 6.7e-7   401 -> 418 us
+//   2048 x 4096 x 128256   2.9e-6 -> 6.5e-7   1383 -> 1425 us
+//   4096 x 2304 x 256000   1.5e-6 -> 5.7e-7   3030 -> 3183 us
+// (parts of 512: 3e-7, another 3 %).
+constexpr int kSliceSteps = 16;
+enum PickKind : int { PICK_NONE = 0, PICK_WHOLE = 1, PICK_SLICES = 2 };
+template <int PICK>
+constexpr int kPairEpiWarps = PICK == PICK_SLICES ? 8 : 4;
+template <int PICK>
+constexpr int kPairThreads = 64 + 32 * kPairEpiWarps<PICK>;
+
+template <bool DUMP, int S, int PICK>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads<PICK>, 1)
     fwd_lse_pair_kernel(const __grid_constant__ CUtensorMap tmE, const __grid_constant__ CUtensorMap tmCh,
                         const FwdArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -397,9 +423,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   int4* unit_slot = reinterpret_cast<int4*>((reinterpret_cast<uintptr_t>(unit_empty + 2) + 15) & ~uintptr_t(15));
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(unit_slot + 2);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
-  // readers of a published unit: the leader's MMA thread and 4 epilogue
-  // warps, the peer's producer and 4 epilogue warps
-  constexpr uint32_t UNIT_CONSUMERS = 10;
+  // readers of a published unit: the leader's MMA thread and epilogue warps,
+  // the peer's producer and epilogue warps
+  constexpr uint32_t UNIT_CONSUMERS = 2 + 2 * kPairEpiWarps<PICK>;
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -415,7 +441,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 8);  // one arrival per epilogue warp of both CTAs
+      mbar_init(&tempty[b], 2 * kPairEpiWarps<PICK>);  // one arrival per epilogue warp of both CTAs
       mbar_init(&unit_full[b], 1);
       mbar_init(&unit_empty[b], UNIT_CONSUMERS);
     }
@@ -638,28 +664,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         int v0, v1;
         split_range(r, a.n_vtile, a.n_split, v0, v1);
         for (int vt = v0; vt < v1; ++vt) {
-          if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, wc)) goto mma_done;
-          tc_fence_after();
-          const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
-          for (int kb = 0; kb < nkb; ++kb) {
-            if (!mbar_wait(&full[stage], phase, wc)) goto mma_done;
+          for (int kb0 = 0; kb0 < nkb; kb0 += PICK == PICK_SLICES ? kSliceSteps : nkb) {
+            if (!mbar_wait(&tempty[acc], acc_phase ^ 1u, wc)) goto mma_done;
             tc_fence_after();
-            const uint32_t a_addr = smem_u32(sA + stage * A_STAGE_BYTES);
-            const uint32_t b_addr = smem_u32(sB + stage * A_STAGE_BYTES);
+            const uint32_t d_tmem = tmem_base + (uint32_t)(acc * BN);
+            const int kb1 = PICK == PICK_SLICES ? min(nkb, kb0 + kSliceSteps) : nkb;
+            for (int kb = kb0; kb < kb1; ++kb) {
+              if (!mbar_wait(&full[stage], phase, wc)) goto mma_done;
+              tc_fence_after();
+              const uint32_t a_addr = smem_u32(sA + stage * A_STAGE_BYTES);
+              const uint32_t b_addr = smem_u32(sB + stage * A_STAGE_BYTES);
 #pragma unroll
-            for (int k = 0; k < BK / 16; ++k)
-              umma_bf16_pair(d_tmem, sdesc_sw128(a_addr + k * 32, 16, 1024), sdesc_sw128(b_addr + k * 32, 16, 1024),
-                             IDESC, (kb | k) != 0);
-            umma_commit_pair_mc(&empty[stage], 0x3);
-            if (++stage == S) {
-              stage = 0;
-              phase ^= 1u;
+              for (int k = 0; k < BK / 16; ++k)
+                umma_bf16_pair(d_tmem, sdesc_sw128(a_addr + k * 32, 16, 1024), sdesc_sw128(b_addr + k * 32, 16, 1024),
+                               IDESC, kb != kb0 || k != 0);
+              umma_commit_pair_mc(&empty[stage], 0x3);
+              if (++stage == S) {
+                stage = 0;
+                phase ^= 1u;
+              }
             }
-          }
-          umma_commit_pair_mc(&tfull[acc], 0x3);
-          if (++acc == 2) {
-            acc = 0;
-            acc_phase ^= 1u;
+            umma_commit_pair_mc(&tfull[acc], 0x3);
+            if (++acc == 2) {
+              acc = 0;
+              acc_phase ^= 1u;
+            }
           }
         }
       }
@@ -672,7 +701,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       }
     }
   } else {
-    // ---------------- epilogue: 4 warps per CTA, one TMEM lane (token row) each ----------------
+    // ---------------- epilogue: 4 warps per CTA (PICK_SLICES: 8), one TMEM lane (token row) each ----------------
     const int lane_grp = warp & 3;
     const int row_in_blk = lane_grp * 32 + lane;
     const uint32_t lane_addr = (uint32_t)(lane_grp * 32) << 16;
@@ -692,37 +721,93 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       split_range(r, a.n_vtile, a.n_split, v0, v1);
       const int row = m2 * (2 * BM) + (int)rank * BM + row_in_blk;
       float mrun = -INFINITY, srun = 0.f;
-      RowTargets tg{};
-      if constexpr (PICK) {
-        // the row's first target in this split's columns
+      bool ok = true;
+      if constexpr (PICK == PICK_SLICES) {
+        // this warp's 128 of each tile's columns, and the row's first target
+        // at or behind the first of them
+        const int hsel = (warp - 2) >> 2;
+        RowTargets tg{};
         tg.ids = a.tgt_id + (size_t)row * a.tgt_k;
         tg.w = a.tgt_w + (size_t)row * a.tgt_k;
         tg.n = row < a.N ? a.tgt_k : 0;
-        tg.pos = lower_bound_id(tg.ids, tg.n, v0 * BN);
+        tg.pos = lower_bound_id(tg.ids, tg.n, v0 * BN + hsel * 128);
         tg.load();
-      }
-      bool ok = true;
-      for (int vt = v0; vt < v1; ++vt) {
-        bool ready = mbar_wait(&tfull[acc], acc_phase, wc);
-        if constexpr (PICK) ready = __all_sync(0xffffffffu, ready);  // the picking loop needs all lanes
-        if (!ready) {
-          ok = false;
-          break;
+        for (int vt = v0; vt < v1 && ok; ++vt) {
+          float x[4][32];
+#pragma unroll
+          for (int q = 0; q < 128; ++q) x[q / 32][q % 32] = 0.f;
+#pragma unroll 1
+          for (int kb0 = 0; kb0 < nkb; kb0 += kSliceSteps) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&tfull[acc], acc_phase, wc));  // (the loops below need all lanes)
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              float y[8];
+              tmem_ld8(tmem_base + lane_addr + (uint32_t)(acc * BN + hsel * 128 + c * 8), y);
+#pragma unroll
+              for (int q = 0; q < 8; ++q) x[c / 4][c % 4 * 8 + q] += y[q];
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(acc ? tempty_leader1 : tempty_leader0);
+            if (++acc == 2) {
+              acc = 0;
+              acc_phase ^= 1u;
+            }
+          }
+          if (!ok) break;
+          const int col0 = vt * BN + hsel * 128;
+          // past the other half's targets
+          while (__any_sync(0xffffffffu, tg.next < col0)) {
+            if (tg.next < col0) {
+              ++tg.pos;
+              tg.load();
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (col0 + c * 32 < a.V) lse_fold_columns<true>(x[c], col0 + c * 32, a, mrun, srun, tg);
         }
-        tc_fence_after();
-        lse_fold_tile<DUMP, PICK>(tmem_base + lane_addr + (uint32_t)(acc * BN), vt * BN, row, a, mrun, srun, tg);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(acc ? tempty_leader1 : tempty_leader0);
-        if (++acc == 2) {
-          acc = 0;
-          acc_phase ^= 1u;
+        if (!ok) break;
+        if (row < a.N) {
+          const size_t at = (size_t)(2 * r + hsel) * a.N + row;
+          a.partial[at] = make_float2(mrun, srun);
+          a.dot[at] = tg.dot;
         }
-      }
-      if (!ok) break;
-      if (row < a.N) {
-        a.partial[(size_t)r * a.N + row] = make_float2(mrun, srun);
-        if constexpr (PICK) a.dot[(size_t)r * a.N + row] = tg.dot;
+      } else {
+        RowTargets tg{};
+        if constexpr (PICK) {
+          // the row's first target in this split's columns
+          tg.ids = a.tgt_id + (size_t)row * a.tgt_k;
+          tg.w = a.tgt_w + (size_t)row * a.tgt_k;
+          tg.n = row < a.N ? a.tgt_k : 0;
+          tg.pos = lower_bound_id(tg.ids, tg.n, v0 * BN);
+          tg.load();
+        }
+        for (int vt = v0; vt < v1; ++vt) {
+          bool ready = mbar_wait(&tfull[acc], acc_phase, wc);
+          if constexpr (PICK) ready = __all_sync(0xffffffffu, ready);  // the picking loop needs all lanes
+          if (!ready) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          lse_fold_tile<DUMP, PICK != PICK_NONE>(tmem_base + lane_addr + (uint32_t)(acc * BN), vt * BN, row, a, mrun,
+                                                 srun, tg);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(acc ? tempty_leader1 : tempty_leader0);
+          if (++acc == 2) {
+            acc = 0;
+            acc_phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        if (row < a.N) {
+          a.partial[(size_t)r * a.N + row] = make_float2(mrun, srun);
+          if constexpr (PICK) a.dot[(size_t)r * a.N + row] = tg.dot;
+        }
       }
     }
   }
@@ -898,14 +983,14 @@ size_t fwd_smem_bytes() { return 1024 + (size_t)FWD_STAGES * STAGE_BYTES + 256; 
 size_t fwd_pair_smem_bytes(int stages) { return 1024 + (size_t)stages * PAIR_STAGE_BYTES + 256; }
 
 namespace {
-template <bool DUMP, int S, bool PICK>
+template <bool DUMP, int S, int PICK>
 cudaError_t launch_pair_stages(const CUtensorMap& tmE, const CUtensorMap& tmCh, const FwdArgs& a, int grid,
                                cudaStream_t stream) {
   const size_t smem = fwd_pair_smem_bytes(S);
   cudaError_t e = cudaFuncSetAttribute(fwd_lse_pair_kernel<DUMP, S, PICK>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  fwd_lse_pair_kernel<DUMP, S, PICK><<<grid, NUM_THREADS, smem, stream>>>(tmE, tmCh, a);
+  fwd_lse_pair_kernel<DUMP, S, PICK><<<grid, kPairThreads<PICK>, smem, stream>>>(tmE, tmCh, a);
   return cudaGetLastError();
 }
 }  // namespace
@@ -915,12 +1000,14 @@ cudaError_t launch_pair_stages(const CUtensorMap& tmE, const CUtensorMap& tmCh, 
 // targets to pick always the latter)
 cudaError_t launch_fwd_lse_pair(const CUtensorMap& tmE, const CUtensorMap& tmCh, const FwdArgs& a, int grid,
                                 int stages, cudaStream_t stream) {
-  if (a.tgt_id) return launch_pair_stages<false, PAIR_STAGES_MAX, true>(tmE, tmCh, a, grid, stream);
+  if (a.tgt_id)
+    return a.sliced ? launch_pair_stages<false, PAIR_STAGES_MAX, PICK_SLICES>(tmE, tmCh, a, grid, stream)
+                    : launch_pair_stages<false, PAIR_STAGES_MAX, PICK_WHOLE>(tmE, tmCh, a, grid, stream);
   if (stages == PAIR_STAGES_MAX)
-    return a.dbg_logits ? launch_pair_stages<true, PAIR_STAGES_MAX, false>(tmE, tmCh, a, grid, stream)
-                        : launch_pair_stages<false, PAIR_STAGES_MAX, false>(tmE, tmCh, a, grid, stream);
-  return a.dbg_logits ? launch_pair_stages<true, PAIR_STAGES, false>(tmE, tmCh, a, grid, stream)
-                      : launch_pair_stages<false, PAIR_STAGES, false>(tmE, tmCh, a, grid, stream);
+    return a.dbg_logits ? launch_pair_stages<true, PAIR_STAGES_MAX, PICK_NONE>(tmE, tmCh, a, grid, stream)
+                        : launch_pair_stages<false, PAIR_STAGES_MAX, PICK_NONE>(tmE, tmCh, a, grid, stream);
+  return a.dbg_logits ? launch_pair_stages<true, PAIR_STAGES, PICK_NONE>(tmE, tmCh, a, grid, stream)
+                      : launch_pair_stages<false, PAIR_STAGES, PICK_NONE>(tmE, tmCh, a, grid, stream);
 }
 
 cudaError_t launch_fwd_lse(const CUtensorMap& tmE, const CUtensorMap& tmC, const FwdArgs& a, int grid,

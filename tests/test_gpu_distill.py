@@ -357,3 +357,25 @@ def test_rows_without_a_gradient_may_hold_anything(bf16):
     got = L.distill_backward(*dirty, lse, dl.cuda(), temperature=2.0, deterministic=True, bf16_grads=bf16)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert (got[0][dead] == 0).all() and torch.isfinite(got[1].float()).all()
+
+
+@pytest.mark.parametrize("D", [1016, 1024, 1032, 2048, 4104])
+def test_long_rows_are_summed_in_parts(D):
+    """The lse of one-signed logits, where every truncation of a running sum
+    goes the same way.  A part of 1024 is 65 additions as in forward_bound, each
+    off by at most one step (2 U32) of the part's sum, and the parts' sums make
+    up the logit; they are added rounded to nearest (U32 of the logit each);
+    exp2's argument, exp2 and the sums as in forward_bound."""
+    import torch
+    import linear_cross_entropy_05_b200 as L
+    N, V, K = 130, 700, 3
+    g = torch.Generator().manual_seed(D)
+    E = torch.rand(N, D, generator=g).to(torch.bfloat16)
+    C = (torch.rand(V, D, generator=g) * (64.0 / D)).to(torch.bfloat16)
+    ids, t = torch.randint(0, V, (N, K), generator=g), torch.randn(N, K, generator=g)
+    loss, lse, _, _, _ = reference(E, C, ids, t, 1.0, torch.ones(N))
+    _, got = L.distill_forward(*(x.cuda() for x in (E, C, ids, t)))
+    parts = -(-D // 1024)
+    zmax = np.abs(f64(E) @ f64(C).T).max(axis=1)
+    bound = (65 * 2 + parts + 8 + 2) * U32 * zmax + (96 + 24) * U32
+    assert (np.abs(got.double().cpu().numpy() - lse) <= bound).all()
