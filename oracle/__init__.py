@@ -34,7 +34,9 @@ A matrix product from numpy's BLAS is the one library primitive used.
 
 Parity status: every function here is pinned by tests/test_oracle_pins.py
 (closed forms, invariants, finite differences, a library cross-entropy and
-autograd, brute-force tile liveness and a hand-worked example).
+autograd, brute-force tile liveness and a hand-worked example); distill and
+distill_targets by tests/test_distill_oracle.py (autograd, differences),
+falling_order and sample_row by tests/test_choose_host.py (by hand).
 """
 from __future__ import annotations
 
@@ -47,6 +49,7 @@ __all__ = [
     "bf16_bits_to_f64", "logits", "forward", "forward_f64", "mean_loss",
     "softmax_grad_f64", "backward", "backward_f64", "backward_sampled",
     "tile_live_map", "tile_live_map_f64",
+    "distill_targets", "distill", "falling_order", "sample_row",
 ]
 
 
