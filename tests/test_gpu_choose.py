@@ -295,3 +295,13 @@ def test_refusals():
                 dict(min_p=1.5), dict(min_p=float("nan"))):
         with pytest.raises(L.CCEError):
             L.sample(E, C, u, **bad)
+    with pytest.raises(L.CCEError):
+        L.sample(E, C, u, top_k=5 - 2 ** 32)      # not 5
+
+
+def test_wide_prefixes_of_two_blocks_of_tokens():
+    """More than 256 tokens: fewer bins a row than head_select has threads."""
+    import linear_cross_entropy_05_b200 as L
+    E, C, z, u = make(15, 261, 16, 21001, spread=1.0)
+    for s in (dict(top_p=0.9), dict(top_k=5000, top_p=0.5)):
+        check_draw(L.sample(E.cuda(), C.cuda(), u.cuda(), **s), z, u, s)

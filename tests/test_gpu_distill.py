@@ -379,3 +379,13 @@ def test_long_rows_are_summed_in_parts(D):
     zmax = np.abs(f64(E) @ f64(C).T).max(axis=1)
     bound = (65 * 2 + parts + 8 + 2) * U32 * zmax + (96 + 24) * U32
     assert (np.abs(got.double().cpu().numpy() - lse) <= bound).all()
+
+
+def test_a_second_derivative_is_refused():
+    import torch
+    import linear_cross_entropy_05_b200 as L
+    E, C, ids, t, _ = [x.cuda() for x in make(91, 20, 64, 300, 4)]
+    E.requires_grad_()
+    g, = torch.autograd.grad(L.linear_distillation(E, C, ids, t), E, create_graph=True)
+    with pytest.raises(RuntimeError):
+        g.sum().backward()
