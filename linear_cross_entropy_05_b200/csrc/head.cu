@@ -99,9 +99,10 @@ __device__ __forceinline__ bool row_exact(const HeadArgs& a, int row) {
   return (a.top_p ? a.top_p[row] : a.top_p_all) < 1.f || !((a.min_p ? a.min_p[row] : a.min_p_all) > 0.f);
 }
 
+// (NaN if any is)
 __device__ __forceinline__ float warp_max(float x) {
   float m;
-  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
+  asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
   return m;
 }
 
@@ -315,6 +316,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(HL_THREADS, 1)
         const int n_here = min(32, a.n_rows - row);
         float* dst = a.logits + (size_t)row * a.ld + v;
         const bool in_double = exact[row >> 5] != 0u;  // (for all of the 32)
+        if (v - lane + 32 > vb) {  // V ends inside this group
+#pragma unroll
+          for (int j = 0; j < 32; ++j) x[j] = in ? x[j] : -INFINITY;
+        }
         // lane j keeps column j's maximum and sum
         float my_max = 0.f;
         unsigned my_hi = 0u, my_lo = 0u;
@@ -325,13 +330,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(HL_THREADS, 1)
             float m[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              // -0 becomes +0, so that equal logits have equal keys; NaN becomes
-              // +inf, which marks the row (a NaN's sign, and so its key, is not
-              // defined after an addition)
-              float z = x[j0 + j] + 0.f;
-              z = z == z ? z : INFINITY;
-              if (in && j0 + j < n_here) dst[(size_t)(j0 + j) * a.ld] = z;
-              x[j0 + j] = in ? z : -INFINITY;
+              // -0 becomes +0, so that equal logits have equal keys
+              x[j0 + j] += 0.f;
+              if (in && j0 + j < n_here) dst[(size_t)(j0 + j) * a.ld] = x[j0 + j];
               m[j] = warp_max(x[j0 + j]);
             }
             // double: each exponential in fixed point, units of 2^-51 in two
@@ -349,7 +350,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(HL_THREADS, 1)
                 const float p = ex2_approx(t);
                 // (t is not above -150, nor a number, where d is -inf)
                 e[j] = d < 0.f && t > -150.f ? fmaf(p, fmaf(d, f, -t) * LN2, p) : 0.f;
-                const unsigned ones = __popc(__ballot_sync(0xffffffffu, d == 0.f));
+                const unsigned ones = __ballot_sync(0xffffffffu, d == 0.f);  // (counted below)
                 my_max = lane == j0 + j ? m[j] : my_max;
                 my_hi = lane == j0 + j ? ones : my_hi;
               }
@@ -377,12 +378,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(HL_THREADS, 1)
           }
         }
         if (lane < n_here) {
+          // a NaN becomes +inf, which marks the row (its logits are not looked at then)
+          my_max = my_max == my_max ? my_max : INFINITY;
           const size_t at = (size_t)(row + lane) * a.n_grp + grp;
           a.gmax[at] = my_max;
           // this warp's own sum over the tiles
           const int i = ((warp - 2) * HL_CHUNKS + c / (HL_EPI_WARPS / 4)) * 32 + lane;
           const float old = bin_max[i], top = fmaxf(old, my_max);
-          double mass = (double)my_hi + (double)my_tail;
+          double mass = (double)__popc(my_hi) + (double)my_tail;
           if (in_double) {
             mass = ((double)my_hi * 67108864.0 + (double)my_lo) * (1.0 / 2251799813685248.0);
             a.gmass[at] = mass;
