@@ -339,20 +339,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(HL_THREADS, 1)
             // words, so that a group's 32 are summed exactly by integer
             // reductions.  float: the largest logit's own (1 each) are counted
             // and the others summed apart from them, so that a log-probability
-            // near 0 keeps its relative precision; the product's rounding is
-            // put back
+            // near 0 keeps its relative precision
             if (!in_double) {
               float e[8];
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
-                const float d = x[j0 + j] - m[j], f = scale_f[row + j0 + j];
-                const float t = d * f;
-                const float p = ex2_approx(t);
-                // (t is not above -150, nor a number, where d is -inf)
-                e[j] = d < 0.f && t > -150.f ? fmaf(p, fmaf(d, f, -t) * LN2, p) : 0.f;
-                const unsigned ones = __ballot_sync(0xffffffffu, d == 0.f);  // (counted below)
+                const float d = x[j0 + j] - m[j];
+                const float p = ex2_approx(d * scale_f[row + j0 + j]);
+                const bool below = d < 0.f;
+                e[j] = below ? p : 0.f;
+                const unsigned others = __ballot_sync(0xffffffffu, below);  // (counted below)
                 my_max = lane == j0 + j ? m[j] : my_max;
-                my_hi = lane == j0 + j ? ones : my_hi;
+                my_hi = lane == j0 + j ? others : my_hi;
               }
               const float tail = __shfl_sync(0xffffffffu, warp_sums(e, lane), (lane & 7) * 4);
               my_tail = (lane >> 3) == (j0 >> 3) ? tail : my_tail;
@@ -385,7 +383,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(HL_THREADS, 1)
           // this warp's own sum over the tiles
           const int i = ((warp - 2) * HL_CHUNKS + c / (HL_EPI_WARPS / 4)) * 32 + lane;
           const float old = bin_max[i], top = fmaxf(old, my_max);
-          double mass = (double)__popc(my_hi) + (double)my_tail;
+          double mass = (double)__popc(~my_hi) + (double)my_tail;
           if (in_double) {
             mass = ((double)my_hi * 67108864.0 + (double)my_lo) * (1.0 / 2251799813685248.0);
             a.gmass[at] = mass;

@@ -20,9 +20,9 @@ U32 = 2.0 ** -24
 # there); the largest logit's own is exact and kept apart.  Of the others' sum
 # the relative error is at most
 #   2^-22      ex2's own
-#   45 U32     t = (z - top) c: the difference and c are rounded, and what is put
-#              back of the product's rounding is: 3 U32 |t| ln 2 of 2^t, and
-#              sum |t| ln 2 2^t / sum 2^t <= ln V + 1 < 15
+#   45 U32     t = (z - top) c: the difference, c and the product are rounded,
+#              3 U32 |t| ln 2 of 2^t, and sum |t| ln 2 2^t / sum 2^t <= ln V + 1
+#              < 15
 #   6 U32      the others of a group are summed in six additions
 # and S = 1 + others (where 1 is the largest), so log S is off by at most
 # FLOAT_SUMS * others / S <= FLOAT_SUMS * log S.
