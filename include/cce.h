@@ -341,10 +341,10 @@ typedef enum { CCE_DTYPE_F32 = 0, CCE_DTYPE_BF16 = 1 } cce_dtype_t;
 
 /* Workspace bytes of cce_distill_forward / cce_distill_backward (0 if the
  * sizes or flags are invalid; the forward's also without a usable device):
- * the forward's partials (12 bytes per token and vocabulary split; 24 if D > 1024) and
- * 8 K + 8 bytes per token; the backward's stripes of G (24 KB per token of at
+ * the forward's partials (16 bytes per token and vocabulary split; 32 if D > 1024) and
+ * 8 K + 20 bytes per token; the backward's stripes of G (24 KB per token of at
  * most 16384 and, for few tokens, as many stripes as 128 MB holds), a copy of E,
- * 8 K + 8 bytes per token and, with CCE_BWD_BF16_GRADS, the fp32 sums of dE
+ * 8 K + 20 bytes per token and, with CCE_BWD_BF16_GRADS, the fp32 sums of dE
  * (and of dC if it is accumulated into or N > 16384). */
 CCE_API size_t cce_distill_forward_workspace_size(int64_t N, int64_t D, int64_t V, int64_t K);
 CCE_API size_t cce_distill_backward_workspace_size(int64_t N, int64_t D, int64_t V, int64_t K, unsigned flags);

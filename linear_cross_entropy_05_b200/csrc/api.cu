@@ -417,7 +417,7 @@ bool plan_backward(int64_t N, int64_t D, int64_t V, BwdPlan* p, unsigned flags =
 struct TargetBuffers {
   int* id;
   float* w;
-  float* neg_entropy;
+  double2* stats;
   int* row_kind;
   int K;
   bool sliced;               // forward
@@ -431,7 +431,7 @@ struct TargetBuffers {
 // weight x logit going to `dot`.
 cce_status_t launch_logit_pass(const void* E, const void* C, int64_t N, int64_t D, int64_t V, const FwdPlan& p,
                                void* ws, float* dbg_logits, cudaStream_t stream, const TargetBuffers* tg = nullptr,
-                               float* dot = nullptr, float scale2 = LOG2E) {
+                               double* dot = nullptr, float scale2 = LOG2E) {
   CUtensorMap tmE, tmC;
   if (!make_map(&tmE, E, N, D, BM) || !make_map(&tmC, C, V, D, p.pair ? BM : BN)) return CCE_ERR_CUDA;
 
@@ -1072,7 +1072,7 @@ bool distill_sizes_ok(int64_t N, int64_t D, int64_t V, int64_t K) {
   return sizes_ok(N, D, V) && V <= INT_MAX - 2 * BN && K > 0 && K <= kMaxTargets && N * K <= (int64_t)1 << 40;
 }
 
-// Workspace: status | forward: partials, split sums | row kinds | entropies |
+// Workspace: status | forward: partials, split sums | row kinds | entropies, sums of weights |
 // sorted ids | weights | backward: E without dead rows, fp32 sums of bf16
 // outputs, stripes.
 struct DistillLayout {
@@ -1087,7 +1087,7 @@ struct DistillLayout {
 void plan_targets(int64_t N, int64_t K, size_t at, DistillLayout* L) {
   L->off_kind = at;
   L->off_ent = L->off_kind + align_up((size_t)N * 4, 256);
-  L->off_id = L->off_ent + align_up((size_t)N * 4, 256);
+  L->off_id = L->off_ent + align_up((size_t)N * 16, 256);
   L->off_w = L->off_id + align_up((size_t)N * K * 4, 256);
   L->bytes = L->off_w + align_up((size_t)N * K * 4, 256);
 }
@@ -1097,7 +1097,7 @@ bool plan_distill_forward(int64_t N, int64_t D, int64_t V, int64_t K, DistillLay
   L->sliced = D > kWholeD;
   L->n_part = L->fwd.n_split * (L->sliced ? 2 : 1);
   L->off_dot = STATUS_BYTES + align_up((size_t)L->n_part * N * sizeof(float2), 256);
-  plan_targets(N, K, L->off_dot + align_up((size_t)L->n_part * N * 4, 256), L);
+  plan_targets(N, K, L->off_dot + align_up((size_t)L->n_part * N * 8, 256), L);
   return true;
 }
 
@@ -1138,7 +1138,7 @@ cce_status_t prepare_targets(const int64_t* ids, const void* teacher, int teache
                              TargetBuffers* tg, cudaStream_t stream, const void* E = nullptr, int64_t D = 0) {
   tg->id = reinterpret_cast<int*>(ws + L.off_id);
   tg->w = reinterpret_cast<float*>(ws + L.off_w);
-  tg->neg_entropy = reinterpret_cast<float*>(ws + L.off_ent);
+  tg->stats = reinterpret_cast<double2*>(ws + L.off_ent);
   tg->row_kind = reinterpret_cast<int*>(ws + L.off_kind);
   tg->K = (int)K;
   TargetArgs t{};
@@ -1152,7 +1152,7 @@ cce_status_t prepare_targets(const int64_t* ids, const void* teacher, int teache
   t.teacher_bf16 = teacher_dtype == CCE_DTYPE_BF16 ? 1 : 0;
   t.tgt_id = tg->id;
   t.tgt_w = tg->w;
-  t.neg_entropy = tg->neg_entropy;
+  t.stats = tg->stats;
   t.row_kind = tg->row_kind;
   t.D = (int)D;
   t.E = E;
@@ -1197,7 +1197,7 @@ cce_status_t cce_distill_forward(const void* E, const void* C, const int64_t* id
   TargetBuffers tg{};
   cce_status_t st = prepare_targets(ids, teacher, teacher_dtype, N, V, K, ignore_index, temperature, ws, L, &tg, stream);
   if (st != CCE_OK) return st;
-  float* dot = reinterpret_cast<float*>(ws + L.off_dot);
+  double* dot = reinterpret_cast<double*>(ws + L.off_dot);
   tg.sliced = L.sliced;
   st = launch_logit_pass(E, C, N, D, V, L.fwd, ws, nullptr, stream, &tg, dot, LOG2E / temperature);
   if (st != CCE_OK) return st;
@@ -1207,7 +1207,7 @@ cce_status_t cce_distill_forward(const void* E, const void* C, const int64_t* id
   f.temperature = temperature;
   f.partial = reinterpret_cast<const float2*>(ws + STATUS_BYTES);
   f.dot = dot;
-  f.neg_entropy = tg.neg_entropy;
+  f.stats = tg.stats;
   f.row_kind = tg.row_kind;
   f.status = reinterpret_cast<unsigned long long*>(ws);
   f.loss = loss;

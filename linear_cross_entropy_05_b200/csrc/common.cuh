@@ -81,7 +81,7 @@ struct FwdArgs {
   const int* tgt_id;   // [N][tgt_k] ascending, absent entries last as INT_MAX
   const float* tgt_w;  // [N][tgt_k]
   int tgt_k;
-  float* dot;          // [n_split][N]
+  double* dot;         // [n_split][N]
   // 1: logits are summed in parts of D, and each split leaves two partials
   // (and two dots), for the halves of its tiles: [2 n_split][N]
   int sliced;
@@ -112,7 +112,7 @@ struct TargetArgs {
   int teacher_bf16;
   int* tgt_id;          // [N][K] out: ids in ascending order, INT_MAX past the last
   float* tgt_w;         // [N][K] out: the teacher's probabilities in that order
-  float* neg_entropy;   // [N] out: sum_k p_k log p_k
+  double2* stats;       // [N] out: sum_k p_k log p_k, and the sum of tgt_w (not quite 1)
   int* row_kind;        // [N] out: RowKind
   // backward: E [N][D] and its copy with zeros in the rows that are not
   // ROW_LIVE, whose NaN or inf must not reach dC = G^T E as 0 * NaN
@@ -125,8 +125,8 @@ struct DistillFinArgs {
   int N, n_part;
   float temperature;
   const float2* partial;     // [n_part][N]
-  const float* dot;          // [n_part][N]
-  const float* neg_entropy;  // [N]
+  const double* dot;         // [n_part][N]
+  const double2* stats;      // [N]
   const int* row_kind;       // [N]
   unsigned long long* status;  // (word ST_NEXT_TILE counts finished blocks)
   float* loss;

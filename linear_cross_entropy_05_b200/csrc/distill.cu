@@ -8,7 +8,7 @@
 //   dloss / dz_v = T (exp(z_v / T - lse) - sum_{k: id_k = v} p_k)
 // An entry is live unless its id is ignore_index or its logit -inf.  The
 // teacher's side costs N K (8 + 4) bytes, nothing beside the logit pass; it
-// is kept in double (sums and exponentials) and rounded once to float.
+// is kept in double; the weights are rounded to float once.
 //
 // distill_targets  one block per row: p, sum p log p, and the entries sorted
 //                  by id, so that the logit and gradient tiles, which walk
@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(256) distill_targets_kernel(const TargetArgs a
   if (tid == 0) {
     a.row_kind[row] = kind;
     if (bad) atomicOr(a.status + ST_FLAGS, SF_BAD_LABEL);
-    if (kind != ROW_LIVE) a.neg_entropy[row] = 0.f;
+    if (kind != ROW_LIVE) a.stats[row] = make_double2(0.0, 0.0);
   }
   if (a.E_live) {
     const uint4* src = reinterpret_cast<const uint4*>(a.E) + (size_t)row * (a.D / 8);
@@ -113,7 +113,6 @@ __global__ void __launch_bounds__(256) distill_targets_kernel(const TargetArgs a
   }
   s = block_reduce<false>(s, buf);
   sxw = block_reduce<false>(sxw, buf);
-  if (tid == 0) a.neg_entropy[row] = (float)(sxw / s - log(s));
 
   // bitonic sort by id (then position)
   for (int size = 2; size <= n_sort; size <<= 1) {
@@ -133,12 +132,17 @@ __global__ void __launch_bounds__(256) distill_targets_kernel(const TargetArgs a
   }
   __syncthreads();
   const double inv = 1.0 / s;
+  double sum_w = 0.0;
   for (int k = tid; k < a.K; k += blockDim.x) {
     const unsigned long long kk = key[k];
     const double x = sx[(unsigned)kk & 0xffffu];
     a.tgt_id[base + k] = (int)(kk >> 32);
-    a.tgt_w[base + k] = x == -INFINITY ? 0.f : (float)(exp(x - top) * inv);
+    const float w = x == -INFINITY ? 0.f : (float)(exp(x - top) * inv);
+    a.tgt_w[base + k] = w;
+    sum_w += (double)w;
   }
+  sum_w = block_reduce<false>(sum_w, buf);
+  if (tid == 0) a.stats[row] = make_double2(sxw / s - log(s), sum_w);
 }
 
 __global__ void __launch_bounds__(32 * FIN_PARTS) distill_finalize_kernel(const DistillFinArgs a) {
@@ -154,7 +158,7 @@ __global__ void __launch_bounds__(32 * FIN_PARTS) distill_finalize_kernel(const 
   if (row < a.N) {
     for (int r = part; r < a.n_part; r += FIN_PARTS) {
       const float2 p = a.partial[(size_t)r * a.N + row];
-      dot += (double)a.dot[(size_t)r * a.N + row];
+      dot += a.dot[(size_t)r * a.N + row];
       const float m = fmaxf(M, p.x);
       if (m != -INFINITY) s = s * exp2f((M - m) * scale2) + p.y * exp2f((p.x - m) * scale2);
       M = m;
@@ -176,8 +180,10 @@ __global__ void __launch_bounds__(32 * FIN_PARTS) distill_finalize_kernel(const 
     const double L = (double)M / T + log((double)s);
     const int kind = a.row_kind[row];
     double loss = 0.0;
-    if (kind == ROW_LIVE)
-      loss = T * T * ((double)a.neg_entropy[row] - dot / T + L);
+    // (lse is weighted by the rounded weights too: their rounding then meets
+    // log-probabilities and not logits)
+    const double2 st = a.stats[row];
+    if (kind == ROW_LIVE) loss = T * T * (st.x - dot / T + st.y * L);
     float lse = (float)L, out = (float)loss;
     if (kind == ROW_BAD) out = __int_as_float(0x7fc00000);
     // a bounded wait gave up: some partials may be an earlier call's

@@ -50,7 +50,7 @@ struct RowTargets {
   const float* w;
   int pos, n;
   int next;    // id of the next target, INT_MAX after the last
-  float dot;   // sum of weight x logit so far
+  double dot;  // sum of weight x logit so far (a loss may be a millionth of it)
   __device__ __forceinline__ void load() { next = pos < n ? __ldg(ids + pos) : INT_MAX; }
 };
 
@@ -66,7 +66,7 @@ __device__ __forceinline__ void lse_fold_columns(float (&x)[32], int cbase, cons
 #pragma unroll
       for (int j = 0; j < 32; ++j) z = (j == at) ? x[j] : z;
       if (at < 32) {
-        tg.dot = fmaf(__ldg(tg.w + tg.pos), z, tg.dot);
+        tg.dot = fma((double)__ldg(tg.w + tg.pos), (double)z, tg.dot);
         ++tg.pos;
         tg.load();
       }

@@ -63,13 +63,13 @@ def test_backward_workspace(L):
     size = L.cce_distill_backward_workspace_size
     N, D, V, K = 8192, 2304, 256000, 64
     stripes = (L.cce_backward_workspace_size_ex(N, D, V, 16) - L.cce_backward_workspace_size(N, D, V))
-    base = 256 + 2 * up(4 * N) + 2 * up(4 * N * K) + up(2 * N * D) + stripes
+    base = 256 + up(4 * N) + up(16 * N) + 2 * up(4 * N * K) + up(2 * N * D) + stripes
     assert size(N, D, V, K, 0) == size(N, D, V, K, 1) == size(N, D, V, K, 4) == base
     assert size(N, D, V, K, 2) == base + up(4 * N * D)                        # dC is rounded where it is formed
     assert size(N, D, V, K, 6) == base + up(4 * N * D) + up(4 * V * D)        # accumulated: fp32 sums first
     assert size(N, D, V, 0, 0) == 0 and size(N, D, V, 1025, 0) == 0 and size(N, D, V, K, 16) == 0
     # few dE tiles: narrower stripes, as many columns of buffers
-    assert size(256, 256, 4096, 8, 0) == 256 + 2 * up(4 * 256) + 2 * up(4 * 256 * 8) + \
+    assert size(256, 256, 4096, 8, 0) == 256 + up(4 * 256) + up(16 * 256) + 2 * up(4 * 256 * 8) + \
         up(2 * 256 * 256) + up(8 + 4 * (16 + 16 + 16 + 1) + 16) + up(16 * 256 * 256 * 2)
     big = size(16385, 256, 4096, 4, 2)
     assert big >= up(4 * 16385 * 256) + up(4 * 4096 * 256)                    # several launches: fp32 sums first
