@@ -32,7 +32,7 @@
 // fixed point, so that no order of summation shows), because float sums would
 // move the borders between tokens by more than a rare token's own width.  Rows
 // whose token does not hang on them (row_exact) take float exponentials
-// (head_logits, 193 tokens x 896 x 151936: 100 us; in double 142 us).
+// (head_logits, 193 tokens x 896 x 151936: 92 us; in double 142 us).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
