@@ -288,10 +288,11 @@ def test_other_streams_graphs_and_two_calls_at_once():
         assert torch.equal(loss, want) and torch.equal(gE, grads[0]) and torch.equal(gC, grads[1])
 
 
-def test_a_wait_that_gives_up_yields_nan():
+@pytest.mark.parametrize("D", [256, 1032])
+def test_a_wait_that_gives_up_yields_nan(D):
     import torch
     import linear_cross_entropy_05_b200 as L
-    E, C, ids, t, dl = [x.cuda() for x in make(61, 300, 256, 5000, 20)]
+    E, C, ids, t, dl = [x.cuda() for x in make(61, 300, D, 5000, 20)]
     ws = L.Workspace("cuda")
     L.cce_debug_set_wait_limit_ns(20_000_000)
     L.cce_debug_withhold_loads(True)
