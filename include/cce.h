@@ -345,7 +345,8 @@ typedef enum { CCE_DTYPE_F32 = 0, CCE_DTYPE_BF16 = 1 } cce_dtype_t;
  * 8 K + 20 bytes per token; the backward's stripes of G (24 KB per token of at
  * most 16384 and, for few tokens, as many stripes as 128 MB holds), a copy of E,
  * 8 K + 20 bytes per token and, with CCE_BWD_BF16_GRADS, the fp32 sums of dE
- * (and of dC if it is accumulated into or N > 16384). */
+ * (and of dC if it is accumulated into or N > 16384); with
+ * CCE_BWD_DETERMINISTIC and few tokens, up to 39 MB of parts of dE. */
 CCE_API size_t cce_distill_forward_workspace_size(int64_t N, int64_t D, int64_t V, int64_t K);
 CCE_API size_t cce_distill_backward_workspace_size(int64_t N, int64_t D, int64_t V, int64_t K, unsigned flags);
 
@@ -368,7 +369,7 @@ CCE_API cce_status_t cce_distill_forward(const void* E, const void* C, const int
  * through stripes of G as with CCE_BWD_STRIPES (no entry is filtered).  What
  * E, lse and dloss hold for a row without a gradient is not looked at.  lse is
  * cce_distill_forward's on the same inputs and temperature.  flags:
- * CCE_BWD_DETERMINISTIC (dE summed in stripe order), CCE_BWD_BF16_GRADS,
+ * CCE_BWD_DETERMINISTIC (dE summed in stripe order; dC always is), CCE_BWD_BF16_GRADS,
  * CCE_BWD_ACCUMULATE, with their meaning in cce_backward_ex. */
 CCE_API cce_status_t cce_distill_backward(const void* E, const void* C, const int64_t* ids, const void* teacher,
                                           int teacher_dtype, const float* lse, const float* dloss,

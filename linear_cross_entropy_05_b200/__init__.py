@@ -236,8 +236,8 @@ def linear_cross_entropy(E, C, y, ignore_index: int = IGNORE_INDEX, filter_eps: 
 def linear_distillation(E, C, ids, teacher, temperature: float = 1.0, ignore_index: int = IGNORE_INDEX):
     """Mean distillation loss (distill_forward) over the tokens that have a
     teacher entry, with autograd support for E and C (bf16 gradients, each
-    sum rounded once); the N x V logits are never stored.  A step that is to be
-    captured into a CUDA graph calls distill_forward and distill_backward."""
+    sum rounded once, and in an order that does not depend on timing); the N x V
+    logits are never stored.  A step that is to be captured into a CUDA graph calls distill_forward and distill_backward."""
     from ._autograd import LinearDistillation
     return LinearDistillation.apply(E, C, ids, teacher, temperature, ignore_index)
 

@@ -39,7 +39,8 @@ class LinearCrossEntropy(torch.autograd.Function):
 
 class LinearDistillation(torch.autograd.Function):
     """Mean distillation loss over the tokens with a teacher entry; the
-    forward keeps the log-sum-exp (N floats) for the backward pass."""
+    forward keeps the log-sum-exp (N floats) for the backward pass, which sums
+    in a fixed order: the same inputs give the same gradients."""
 
     @staticmethod
     def forward(ctx, E, C, ids, teacher, temperature: float, ignore_index: int):
@@ -56,6 +57,6 @@ class LinearDistillation(torch.autograd.Function):
     def backward(ctx, g):
         E, C, ids, teacher, lse, inv_count = ctx.saved_tensors
         dE, dC = _distill_backward(E, C, ids, teacher, lse, g.to(torch.float32), ctx.temperature, ctx.ignore_index,
-                                   bf16_grads=True, dloss_scale=inv_count)
+                                   bf16_grads=True, deterministic=True, dloss_scale=inv_count)
         need = ctx.needs_input_grad
         return dE if need[0] else None, dC if need[1] else None, None, None, None, None

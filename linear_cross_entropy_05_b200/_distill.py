@@ -135,11 +135,12 @@ def distill_backward(E, C, ids, teacher, lse, dloss, temperature: float = 1.0, i
     or bf16 with bf16_grads.  dloss is [N], or a scalar tensor for all rows;
     dloss_scale, a scalar tensor, multiplies it (with distill_forward's second
     mean: the gradient of dloss times the mean).  deterministic=True sums dE in
-    a fixed order; accumulate=True adds to the tensors given in `out`
+    a fixed order (linear_distillation does); accumulate=True adds to the tensors given in `out`
     (required).  The
     logits are formed again on chip; the scratch is 24 KB per token (of at most
     16384) or, for few tokens, up to 128 MB, a copy of E, and the fp32 sums of
-    dE for bf16 outputs (and of dC with accumulate or more than 16384 tokens).
+    dE for bf16 outputs (and of dC with accumulate or more than 16384 tokens);
+    with deterministic and few tokens, up to 39 MB of parts of dE.
     What E, lse and dloss hold for a row without entries is not looked at."""
     N, D, V = check_head(E, C)
     K, dtype = _check_targets(ids, teacher, N, E.device)

@@ -47,6 +47,8 @@ cudaError_t launch_flat_rows(const void* E, const void* C, const int64_t* y, con
 cudaError_t launch_f32_to_bf16(const float* src, void* dst, size_t n, bool accumulate, int sms, cudaStream_t stream);
 cudaError_t launch_distill_targets(const TargetArgs& a, cudaStream_t stream);
 cudaError_t launch_distill_finalize(const DistillFinArgs& a, cudaStream_t stream);
+cudaError_t launch_distill_parts(const float* parts, int n_parts, size_t part_floats, void* out, size_t n, bool bf16,
+                                 bool accumulate, int sms, cudaStream_t stream);
 int head_logits_stages(int nt);
 cudaError_t launch_head_logits(const CUtensorMap& tmC, const CUtensorMap& tmC32, const CUtensorMap& tmE,
                                const HeadArgs& a, int grid, cudaStream_t stream);
@@ -313,6 +315,7 @@ std::atomic<int> g_stripe_lag{2};    // interleaved order: groups between A and 
 
 struct StripeLayout {
   StripePlan p;          // of a full super-block
+  int dE_parts;          // (see StripeArgs)
   int n_sb;              // super-blocks (launches)
   int Ns_pad, Vs;
   size_t off_ctr, ctr_bytes, off_G, G_bytes, bytes;
@@ -326,8 +329,14 @@ struct StripeLayout {
 // holds, so that a few tokens' stripes, whose tasks do not fill the GPU, do not
 // wait for one another (6 tokens x 744 x 180434: 802 us with three buffers,
 // 460 us with all 45).
+// parts (deterministic distillation): where a stripe has fewer dE-tile tasks
+// than two for each pair, tasks of several stripes run side by side; their
+// tiles of dE are then formed in so many parts that these do not wait for one
+// another (at most 148 tiles of 256 KB, 39 MB).  One part against so many, and
+// against sums in any order, us: 256 x 256 x 4096 126, 51, 53; 7 x 192 x 23568
+// 345, 90, 84; 1000 x 2040 x 100003 1342, 1293, 1295.
 constexpr size_t kStripeRoom = size_t(128) << 20;
-StripeLayout plan_stripes(int64_t N, int64_t D, int64_t V, size_t base, int narrow_pairs = 0) {
+StripeLayout plan_stripes(int64_t N, int64_t D, int64_t V, size_t base, int narrow_pairs = 0, bool parts = false) {
   StripeLayout L{};
   const int n_m2_total = (int)((N + 255) / 256);
   L.p.n_m2 = std::min(n_m2_total, kStripeMaxM2);
@@ -351,7 +360,12 @@ StripeLayout plan_stripes(int64_t N, int64_t D, int64_t V, size_t base, int narr
   L.n_doneA_v = (size_t)L.p.n_vtile;
   L.n_doneA_ms = (size_t)L.p.n_s * L.p.n_m2;
   L.n_doneBC = (size_t)L.p.n_s;
-  L.n_doneC = (size_t)L.p.n_m2 * L.p.n_dc;
+  L.dE_parts = 1;
+  if (parts) {
+    const int64_t tiles = (int64_t)n_m2_total * L.p.n_dc;
+    L.dE_parts = (int)std::min<int64_t>(L.p.n_s, (2 * narrow_pairs + tiles - 1) / tiles);
+  }
+  L.n_doneC = (size_t)L.dE_parts * L.p.n_m2 * L.p.n_dc;
   L.off_ctr = base;
   L.n_nz = (size_t)L.p.n_s * L.p.n_m2 * L.p.vt_per_s;
   L.ctr_bytes = align_up(8 + 4 * (L.n_doneA_v + L.n_doneA_ms + L.n_doneBC + L.n_doneC) + L.n_nz, 256);
@@ -694,6 +708,9 @@ cce_status_t cce_debug_set_kernel_events(int kernel, void* start_event, void* st
 
 namespace {
 
+// Rows from one part of dE to the next (whole boxes of 32).
+int64_t part_rows(int64_t N) { return (N + 31) / 32 * 32; }
+
 // Dense backward through softmax-gradient stripes (bwd_stripe.cu): one
 // launch per token super-block; a: the common backward arguments.
 cce_status_t backward_stripes(const void* E, const void* C, void* dE, void* dC, const BwdPlan& bp, const BwdArgs& a,
@@ -707,7 +724,8 @@ cce_status_t backward_stripes(const void* E, const void* C, void* dE, void* dC, 
   if (!make_map(&maps[0], E, a.N, a.D, 128) || !make_map(&maps[1], C, a.V, a.D, 128) ||
       !make_map(&maps[2], G, Grows, L.Vs, 32) || !make_map(&maps[3], G, Grows, L.Vs, 128) ||
       !make_map(&maps[4], G, Grows, L.Vs, 64) || !make_map(&maps[5], E, a.N, a.D, 64) ||
-      !make_map(&maps[6], C, a.V, a.D, 64) || !make_map_f32(&maps[7], dE, a.N, a.D) ||
+      !make_map(&maps[6], C, a.V, a.D, 64) ||
+      !make_map_f32(&maps[7], dE, L.dE_parts > 1 ? L.dE_parts * part_rows(a.N) : a.N, a.D) ||
       !(dC_bf16 ? make_map(&maps[8], dC, a.V, a.D, 32) : make_map_f32(&maps[8], dC, a.V, a.D)))
     return CCE_ERR_CUDA;
   // (where D is not a multiple of 64 the last group would reach past the rows' ends)
@@ -747,6 +765,8 @@ cce_status_t backward_stripes(const void* E, const void* C, void* dE, void* dC, 
     sa.dC_bf16 = dC_bf16 ? 1 : 0;
     sa.wide_boxes = wide_boxes ? 1 : 0;
   }
+  sa.dE_parts = L.dE_parts;
+  sa.dE_part_rows = (int)part_rows(a.N);
   sa.ordered = ordered ? 1 : 0;
   sa.status = a.status;
   sa.wait_limit_ns = a.wait_limit_ns;
@@ -1074,7 +1094,7 @@ bool distill_sizes_ok(int64_t N, int64_t D, int64_t V, int64_t K) {
 
 // Workspace: status | forward: partials, split sums | row kinds | entropies, sums of weights |
 // sorted ids | weights | backward: E without dead rows, fp32 sums of bf16
-// outputs, stripes.
+// outputs or the parts of dE, stripes.
 struct DistillLayout {
   FwdPlan fwd;        // forward only
   bool sliced;        // (see PICK_SLICES)
@@ -1116,15 +1136,17 @@ bool plan_distill_backward(int64_t N, int64_t D, int64_t V, int64_t K, unsigned 
   const int64_t per_launch = 256 * (int64_t)std::max(1, std::min(kStripeMaxM2, g_stripe_m2.load()));
   L->dC_direct = bf16 && !(flags & CCE_BWD_ACCUMULATE) && N <= per_launch;
   L->off_dE32 = L->off_dC32 = 0;
-  if (bf16) {
+  const bool ordered = (flags & CCE_BWD_DETERMINISTIC) != 0;
+  const int parts = plan_stripes(N, D, V, 0, kNarrowPairs, ordered).dE_parts;
+  if (bf16 || parts > 1) {
     L->off_dE32 = L->bytes;
-    L->bytes += align_up((size_t)N * D * 4, 256);
-    if (!L->dC_direct) {
-      L->off_dC32 = L->bytes;
-      L->bytes += align_up((size_t)V * D * 4, 256);
-    }
+    L->bytes += align_up(parts > 1 ? (size_t)(parts * part_rows(N)) * D * 4 : (size_t)N * D * 4, 256);
   }
-  L->stripes = plan_stripes(N, D, V, L->bytes, kNarrowPairs);
+  if (bf16 && !L->dC_direct) {
+    L->off_dC32 = L->bytes;
+    L->bytes += align_up((size_t)V * D * 4, 256);
+  }
+  L->stripes = plan_stripes(N, D, V, L->bytes, kNarrowPairs, ordered);
   L->bytes = L->stripes.bytes;
   return true;
 }
@@ -1247,10 +1269,13 @@ cce_status_t cce_distill_backward(const void* E, const void* C, const int64_t* i
   const bool bf16 = (flags & CCE_BWD_BF16_GRADS) != 0;
   const bool accumulate = (flags & CCE_BWD_ACCUMULATE) != 0;
   // fp32 sums: the outputs themselves, or scratch rounded once at the end
-  float* dE32 = bf16 ? reinterpret_cast<float*>(ws + L.off_dE32) : reinterpret_cast<float*>(dE);
+  // (parts: stored first, then added to; summed at the end)
+  const int parts = L.stripes.dE_parts;
+  float* dE32 = bf16 || parts > 1 ? reinterpret_cast<float*>(ws + L.off_dE32) : reinterpret_cast<float*>(dE);
   void* dC_sum = bf16 && !L.dC_direct ? static_cast<void*>(ws + L.off_dC32) : dC;
   const bool acc32 = accumulate && !bf16;
-  if (!acc32 && cudaMemsetAsync(dE32, 0, (size_t)N * D * sizeof(float), stream) != cudaSuccess) return CCE_ERR_CUDA;
+  if (!acc32 && parts == 1 && cudaMemsetAsync(dE32, 0, (size_t)N * D * sizeof(float), stream) != cudaSuccess)
+    return CCE_ERR_CUDA;
   BwdPlan bp{};
   bp.stripes = L.stripes;
   BwdArgs a{};
@@ -1269,9 +1294,16 @@ cce_status_t cce_distill_backward(const void* E, const void* C, const int64_t* i
   tg.dloss_scale = dloss_scale;
   st = backward_stripes(ws + L.off_E, C, dE32, dC_sum, bp, a, acc32, (flags & CCE_BWD_DETERMINISTIC) != 0, di.sms, ws, stream,
                         nullptr, &tg, temperature, L.dC_direct);
-  if (st != CCE_OK || !bf16) return st;
-  if (launch_f32_to_bf16(dE32, dE, (size_t)N * D, accumulate, di.sms, stream) != cudaSuccess) return CCE_ERR_CUDA;
-  if (!L.dC_direct && launch_f32_to_bf16(reinterpret_cast<const float*>(dC_sum), dC, (size_t)V * D, accumulate,
+  if (st != CCE_OK) return st;
+  if (parts > 1) {
+    if (launch_distill_parts(dE32, parts, (size_t)part_rows(N) * D, dE, (size_t)N * D, bf16, accumulate, di.sms,
+                             stream) != cudaSuccess)
+      return CCE_ERR_CUDA;
+  } else if (bf16 &&
+             launch_f32_to_bf16(dE32, dE, (size_t)N * D, accumulate, di.sms, stream) != cudaSuccess) {
+    return CCE_ERR_CUDA;
+  }
+  if (bf16 && !L.dC_direct && launch_f32_to_bf16(reinterpret_cast<const float*>(dC_sum), dC, (size_t)V * D, accumulate,
                                          di.sms, stream) != cudaSuccess)
     return CCE_ERR_CUDA;
   return CCE_OK;

@@ -743,16 +743,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SP_THREADS, 1)
         const int row0 = isB ? t.a * BN + r * 128 + lg * 32 : a.tok0 + t.a * 256 + r * 128 + lg * 32;
         const int rows_lim = isB ? a.V : a.N;
         const CUtensorMap* map = isB ? &mp.dC : &mp.dE;
-        const bool add = isB ? (a.dC_add != 0) : true;
+        const int n_parts = PICK ? a.dE_parts : 1;
+        const int part = isB || n_parts == 1 ? 0 : t.s % n_parts;
+        const bool add = isB ? (a.dC_add != 0) : n_parts == 1 || t.s >= n_parts;
+        const int row_out = row0 + (n_parts == 1 ? 0 : part * a.dE_part_rows);
         const int nd = chunk_width(a.D, t.b);
-        unsigned* tile_ctr = isB ? nullptr : a.doneC + (size_t)t.a * P.n_dc + t.b;
-        if (!isB && a.ordered && t.s > 0) {
+        unsigned* tile_ctr = isB ? nullptr : a.doneC + ((size_t)part * P.n_m2 + t.a) * P.n_dc + t.b;
+        if (!isB && a.ordered && t.s >= n_parts) {
           // Ordered mode: this dE tile's reduce-adds follow those of the
-          // previous stripe, so every entry is summed in stripe order and the
-          // result does not depend on timing (bitwise reproducible).
+          // previous stripe (of its part), so every entry is summed in stripe
+          // order and the result does not depend on timing (bitwise
+          // reproducible).
           int ok = 1;
           if (lane == 0) {
-            const unsigned want = SP_DONE * (unsigned)t.s;
+            const unsigned want = SP_DONE * (unsigned)(t.s / n_parts);
             if (ld_acquire_gpu(tile_ctr) < want) {
               const uint64_t t0 = global_timer_ns();
               ok = 0;
@@ -832,9 +836,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SP_THREADS, 1)
             __syncwarp();
             if (lane == 0) {
               if (add)
-                tma_reduce_add_2d(map, xb, x0, row0);
+                tma_reduce_add_2d(map, xb, x0, row_out);
               else
-                tma_store_2d(map, xb, x0, row0);
+                tma_store_2d(map, xb, x0, row_out);
               bulk_commit_group();
             }
           }

@@ -421,7 +421,7 @@ struct StripeArgs {
   unsigned* doneA_v;
   unsigned* doneA_ms;
   unsigned* doneBC;
-  unsigned* doneC;       // [n_m2][n_dc] C tasks of each dE tile (ordered mode)
+  unsigned* doneC;       // [dE_parts][n_m2][n_dc] C tasks of each dE tile (ordered mode)
   unsigned long long* next;
   int ordered;           // 1: the stripes' reduce-adds into a dE tile happen in stripe order
   int dE_prefetch;       // 1: dE-tile tasks ask for their dE rows in L2 when they start
@@ -455,6 +455,11 @@ struct StripeArgs {
   const float* dloss_scale;  // optional: a factor of every dloss
   int wide_boxes;        // 1: E and C in 128-column boxes too (D a multiple of 64)
   int dC_bf16;           // 1: dC-tile tasks store bf16 (dC_add = 0; the dC map is of bf16 boxes)
+  // > 1: stripe s forms its share of dE in part s % dE_parts of the dE map
+  // (rows dE_part_rows apart; the first stripe of a part stores, the others
+  // add), so that the ordered mode waits only for stripe s - dE_parts
+  int dE_parts;
+  int dE_part_rows;
 };
 
 // First position of the ascending ids[0 .. n) that is not below `first`.

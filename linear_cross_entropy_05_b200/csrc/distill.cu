@@ -19,6 +19,8 @@
 //                  and loss; 32 rows x 16 split lanes per block, so the
 //                  [split][row] partials are read in whole lines.  The block
 //                  that finishes last adds up the mean, in a fixed order.
+// distill_parts    adds up dE from the parts that few tokens' stripes leave
+//                  (deterministic mode), in the order of the parts.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -215,6 +217,44 @@ __global__ void __launch_bounds__(32 * FIN_PARTS) distill_finalize_kernel(const 
     *a.mean = (float)(sum / n);
     *a.inv_count = (float)(1.0 / n);
   }
+}
+
+// dE = the sum of the parts (plus dE itself with `accumulate`), in their order.
+// part4: float4s from one part to the next.
+__global__ void __launch_bounds__(256) distill_parts_kernel(const float4* __restrict__ parts, int n_parts, size_t part4,
+                                                            void* out, size_t n4, int bf16, int accumulate) {
+  const size_t stride = (size_t)gridDim.x * blockDim.x;
+  for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n4; i += stride) {
+    float4 v = __ldg(parts + i);
+#pragma unroll 8
+    for (int p = 1; p < n_parts; ++p) {
+      const float4 x = __ldg(parts + p * part4 + i);
+      v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
+    }
+    if (!bf16) {
+      float4* dst = reinterpret_cast<float4*>(out) + i;
+      if (accumulate) v = make_float4(v.x + dst->x, v.y + dst->y, v.z + dst->z, v.w + dst->w);
+      *dst = v;
+    } else {
+      uint2* dst = reinterpret_cast<uint2*>(out) + i;
+      if (accumulate) {
+        const uint2 o = *dst;
+        const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&o.x));
+        const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&o.y));
+        v = make_float4(v.x + a.x, v.y + a.y, v.z + b.x, v.w + b.y);
+      }
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+      *dst = make_uint2(*reinterpret_cast<const unsigned*>(&lo), *reinterpret_cast<const unsigned*>(&hi));
+    }
+  }
+}
+
+cudaError_t launch_distill_parts(const float* parts, int n_parts, size_t part_floats, void* out, size_t n, bool bf16,
+                                 bool accumulate, int sms, cudaStream_t stream) {
+  const size_t blocks = (n / 4 + 255) / 256;
+  distill_parts_kernel<<<(unsigned)(blocks < (size_t)sms * 8 ? blocks : (size_t)sms * 8), 256, 0, stream>>>(
+      reinterpret_cast<const float4*>(parts), n_parts, part_floats / 4, out, n / 4, bf16 ? 1 : 0, accumulate ? 1 : 0);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_distill_targets(const TargetArgs& a, cudaStream_t stream) {

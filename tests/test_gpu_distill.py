@@ -390,3 +390,48 @@ def test_a_second_derivative_is_refused():
     g, = torch.autograd.grad(L.linear_distillation(E, C, ids, t), E, create_graph=True)
     with pytest.raises(RuntimeError):
         g.sum().backward()
+
+
+@pytest.mark.parametrize("N,D,V,K", [(256, 256, 4096, 8), (700, 264, 9001, 17), (1500, 1032, 20011, 4)])
+def test_a_step_repeats_itself(N, D, V, K):
+    import torch
+    import linear_cross_entropy_05_b200 as L
+    E, C, ids, t, _ = [x.cuda() for x in make(101, N, D, V, K)]
+    first = None
+    for _ in range(6):
+        a, b = E.detach().requires_grad_(), C.detach().requires_grad_()
+        loss = L.linear_distillation(a, b, ids, t, temperature=1.5)
+        got = (loss.detach(),) + torch.autograd.grad(loss, (a, b))
+        first = first or got
+        assert all(torch.equal(x, y) for x, y in zip(first, got))
+
+
+@pytest.mark.parametrize("N,D,V", [(1, 8, 300), (7, 192, 23568), (33, 264, 5000), (520, 1032, 60011), (600, 40, 100003)])
+@pytest.mark.parametrize("per_launch", [None, 256])
+def test_the_deterministic_sums_are_the_others(N, D, V, per_launch):
+    """Only the order of fp32 additions of dE differs (one for each stripe, each
+    off by U32 of a partial sum): fp32 gradients agree to 1e-5 of their norm,
+    bf16 ones to the few values that round the other way."""
+    import torch
+    import linear_cross_entropy_05_b200 as L
+    E, C, ids, t, dl = make(111, N, D, V, 3)
+    dev = [x.cuda() for x in (E, C, ids, t)]
+    _, lse = L.distill_forward(*dev)
+    dl = dl.cuda()
+    if per_launch:
+        L.cce_debug_set_stripe_params(tokens_per_launch=per_launch)
+    try:
+        for bf16 in (False, True):
+            for acc in (False, True):
+                gdt = torch.bfloat16 if bf16 else torch.float32
+                runs = []
+                for det in (False, True, True):
+                    out = tuple(torch.full(s, 0.25, dtype=gdt, device="cuda") for s in ((N, D), (V, D)))
+                    runs.append(L.distill_backward(*dev, lse, dl, bf16_grads=bf16, accumulate=acc, deterministic=det,
+                                                   out=out))
+                for a, b, c in zip(*runs):
+                    assert torch.equal(b, c)
+                    a, b = a.float(), b.float()
+                    assert (a - b).norm() <= (U16 if bf16 else 1e-5) * a.norm()
+    finally:
+        L.cce_debug_set_stripe_params()
