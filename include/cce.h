@@ -401,7 +401,8 @@ CCE_API cce_status_t cce_top_logits(const void* E, const void* C, int64_t N, int
 /* Settings of cce_sample: device arrays [N], or, where the pointer is null,
  * the *_all value for every row. */
 typedef struct {
-  const float* temperature; /* > 0, or 0: the largest logit (u and the filters do not matter) */
+  const float* temperature; /* > 0 (infinite: every logit but -inf weighs alike), or 0: the largest
+                               logit (u and the filters do not matter) */
   const int32_t* top_k;     /* the k largest stay; 0 (or >= V): off */
   const float* top_p;       /* the shortest prefix, in falling order, of at least this share of the
                                mass that top_k left (at least one entry); >= 1: off */

@@ -194,7 +194,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(HL_THREADS, 1)
   for (int n = threadIdx.x; n < HEAD_ROWS; n += HL_THREADS) {  // (whole warps)
     const bool live = n < a.n_rows;
     scale[n] = live ? row_scale(a, a.n0 + n) : 1.0;
-    scale_f[n] = (float)scale[n];
+    // (an infinite temperature's 1e-300 would be 0, and -inf * 0 NaN; the least
+    // float makes exp2(d * scale) 1 for every finite d, and 0 for -inf)
+    scale_f[n] = fmaxf((float)scale[n], 1.4e-45f);
     const unsigned bits = __ballot_sync(0xffffffffu, live && row_exact(a, a.n0 + n));
     if (lane == 0) exact[n >> 5] = bits;
   }

@@ -305,3 +305,31 @@ def test_wide_prefixes_of_two_blocks_of_tokens():
     E, C, z, u = make(15, 261, 16, 21001, spread=1.0)
     for s in (dict(top_p=0.9), dict(top_k=5000, top_p=0.5)):
         check_draw(L.sample(E.cuda(), C.cuda(), u.cuda(), **s), z, u, s)
+
+
+@pytest.mark.parametrize("V", [31, 257, 900, 1024, 5003])
+def test_an_infinite_temperature_draws_evenly(V):
+    """x = z / inf: 0 for every logit but one of -inf, which has no weight."""
+    import torch
+    import linear_cross_entropy_05_b200 as L
+    E, C, z, u = make(51, 40, 64, V)
+    E[:, 0] = 0
+    E[7, 0] = 2.0 ** 100
+    C[:, 0] = 0
+    C[[0, V // 2, V - 1], 0] = -(2.0 ** 100)     # these logits of row 7 are -inf
+    z = E.double().numpy() @ C.double().numpy().T
+    z[z < -1e38] = -np.inf
+    live = np.flatnonzero(z[7] > -np.inf)
+    assert live.size == V - 3 and np.isfinite(np.delete(z, 7, 0)).all()
+    inf = float("inf")
+    for s in (dict(top_k=9), dict(top_k=V - 1), dict(min_p=0.5), dict(top_k=20, top_p=0.5), dict(),
+              dict(top_p=0.6), dict(top_k=12, min_p=0.25)):
+        for rows in (False, True):
+            t = torch.full((40,), inf, device="cuda") if rows else inf
+            token, logp = L.sample(E.cuda(), C.cuda(), u.cuda(), temperature=t, **s)
+            keep = np.delete(np.arange(40), 7)
+            check_draw((token[keep], logp[keep]), z[keep], u[keep], dict(temperature=inf, **s))
+            if s.get("top_k", 0) != V - 1:       # row 7 over the entries with any weight
+                at = torch.from_numpy(np.searchsorted(live, token[[7]].cpu().numpy()))
+                assert live[at.item()] == token[7].item()
+                check_draw((at, logp[[7]]), z[[7]][:, live], u[[7]], dict(temperature=inf, **s))
