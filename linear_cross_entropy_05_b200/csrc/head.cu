@@ -1184,12 +1184,13 @@ __device__ int sample_row(const Row& r, const double (&mass)[2], int k, double p
     return draw_from_candidates(r, c, k, p, min_p, u, total, s);
   }
   if (k == 0) {
-    // entries below min_p of the largest are out (a little slack: their own
-    // masses decide); of the others, groups in growing numbers until their
-    // candidates hold p of the mass
+    // entries below min_p of the largest are out (a little slack, in the mass
+    // too, whose rounding is far apart in logits at a large T: their own masses
+    // decide); of the others, groups in growing numbers until their candidates
+    // hold p of the mass
     unsigned floor_key = 0u;
     if (min_p > 0.0) {
-      const double t = (double)r.zmax + log2(min_p) / r.scale;
+      const double t = (double)r.zmax + (log2(min_p) - 0x1p-50) / r.scale;
       floor_key = min(r.top, order_key((float)(t - 1e-6 * (fabs(t) + fabs((double)r.zmax) + 1.0))));
     }
     for (int want = 64; want <= 4096; want <<= 3) {

@@ -333,3 +333,15 @@ def test_an_infinite_temperature_draws_evenly(V):
                 at = torch.from_numpy(np.searchsorted(live, token[[7]].cpu().numpy()))
                 assert live[at.item()] == token[7].item()
                 check_draw((at, logp[[7]]), z[[7]][:, live], u[[7]], dict(temperature=inf, **s))
+
+
+@pytest.mark.parametrize("V", [31, 900, 9001])
+def test_min_p_of_one_at_temperatures_that_level_the_masses(V):
+    """Where exp((z - max) / T) rounds to 1 in double, every entry is as likely
+    as the largest."""
+    import linear_cross_entropy_05_b200 as L
+    E, C, z, u = make(52, 10, 64, V)
+    for t in (1e18, 1e30, float("inf")):
+        for s in (dict(min_p=1.0), dict(min_p=1.0, top_k=12), dict(min_p=1.0, top_p=0.5)):
+            s["temperature"] = t
+            check_draw(L.sample(E.cuda(), C.cuda(), u.cuda(), **s), z, u, s)
