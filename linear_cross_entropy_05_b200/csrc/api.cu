@@ -1221,12 +1221,14 @@ cce_status_t cce_distill_forward(const void* E, const void* C, const int64_t* id
   if (st != CCE_OK) return st;
   double* dot = reinterpret_cast<double*>(ws + L.off_dot);
   tg.sliced = L.sliced;
-  st = launch_logit_pass(E, C, N, D, V, L.fwd, ws, nullptr, stream, &tg, dot, LOG2E / temperature);
+  const float scale2 = LOG2E / temperature;
+  st = launch_logit_pass(E, C, N, D, V, L.fwd, ws, nullptr, stream, &tg, dot, scale2);
   if (st != CCE_OK) return st;
   DistillFinArgs f{};
   f.N = (int)N;
   f.n_part = L.n_part;
   f.temperature = temperature;
+  f.scale2 = scale2;
   f.partial = reinterpret_cast<const float2*>(ws + STATUS_BYTES);
   f.dot = dot;
   f.stats = tg.stats;

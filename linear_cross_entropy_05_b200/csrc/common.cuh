@@ -124,7 +124,8 @@ struct TargetArgs {
 struct DistillFinArgs {
   int N, n_part;
   float temperature;
-  const float2* partial;     // [n_part][N]
+  float scale2;              // as in FwdArgs
+  const float2* partial;     // [n_part][N] (max, sum of 2^(scale2 z) relative to 2^(scale2 max as a float))
   const double* dot;         // [n_part][N]
   const double2* stats;      // [N]
   const int* row_kind;       // [N]

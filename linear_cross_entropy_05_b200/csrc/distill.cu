@@ -149,20 +149,21 @@ __global__ void __launch_bounds__(256) distill_targets_kernel(const TargetArgs a
 
 __global__ void __launch_bounds__(32 * FIN_PARTS) distill_finalize_kernel(const DistillFinArgs a) {
   __shared__ float sm[FIN_PARTS][32];
-  __shared__ float ss[FIN_PARTS][32];
+  __shared__ double ss[FIN_PARTS][32];
   __shared__ double sd[FIN_PARTS][32];
   __shared__ int s_last;
   const int lane = threadIdx.x, part = threadIdx.y;
   const int row = blockIdx.x * 32 + lane;
-  const float scale2 = LOG2E / a.temperature;
-  float M = -INFINITY, s = 0.f;
-  double dot = 0.0;
+  // (sums relative to 2^ms(M): see lse_fold_columns)
+  auto ms = [&](float m) { return __fmul_rn(m, a.scale2); };
+  float M = -INFINITY;
+  double s = 0.0, dot = 0.0;
   if (row < a.N) {
     for (int r = part; r < a.n_part; r += FIN_PARTS) {
       const float2 p = a.partial[(size_t)r * a.N + row];
       dot += a.dot[(size_t)r * a.N + row];
       const float m = fmaxf(M, p.x);
-      if (m != -INFINITY) s = s * exp2f((M - m) * scale2) + p.y * exp2f((p.x - m) * scale2);
+      if (m != -INFINITY) s = s * (double)exp2f(ms(M) - ms(m)) + (double)p.y * (double)exp2f(ms(p.x) - ms(m));
       M = m;
     }
   }
@@ -172,14 +173,16 @@ __global__ void __launch_bounds__(32 * FIN_PARTS) distill_finalize_kernel(const 
   __syncthreads();
   if (part == 0 && row < a.N) {
     for (int q = 1; q < FIN_PARTS; ++q) M = fmaxf(M, sm[q][lane]);
-    s = 0.f;
+    s = 0.0;
     dot = 0.0;
     for (int q = 0; q < FIN_PARTS; ++q) {
-      if (sm[q][lane] != -INFINITY) s += ss[q][lane] * exp2f((sm[q][lane] - M) * scale2);
+      if (sm[q][lane] != -INFINITY) s += ss[q][lane] * (double)exp2f(ms(sm[q][lane]) - ms(M));
       dot += sd[q][lane];
     }
     const double T = (double)a.temperature;
-    const double L = (double)M / T + log((double)s);
+    // M / T, and what the rounding of ms left of the shift
+    constexpr double kLn2 = 0.69314718055994530942;
+    const double L = (double)M / T + kLn2 * ((double)ms(M) - (double)M * (double)a.scale2) + log(s);
     const int kind = a.row_kind[row];
     double loss = 0.0;
     // (lse is weighted by the rounded weights too: their rounding then meets

@@ -435,3 +435,64 @@ def test_the_deterministic_sums_are_the_others(N, D, V, per_launch):
                     assert (a - b).norm() <= (U16 if bf16 else 1e-5) * a.norm()
     finally:
         L.cce_debug_set_stripe_params()
+
+
+def records(z, tiles):
+    """Upper bound, per row, on how often the running maximum of a share of the
+    vocabulary grows: shares are at most `tiles` tiles of 256, folded 32 columns
+    at a time."""
+    N, V = z.shape
+    pad = -V % 256
+    m = np.pad(z, ((0, 0), (0, pad)), constant_values=-np.inf).reshape(N, -1, 32).max(axis=2)
+    most = np.zeros(N, dtype=int)
+    for s in range(0, m.shape[1], 8):
+        run = np.maximum.accumulate(m[:, s:s + 8 * tiles], axis=1)
+        most = np.maximum(most, 1 + (np.diff(run, axis=1) > 0).sum(axis=1))
+    return most
+
+
+@pytest.mark.parametrize("T", [1e-3, 0.05, 1.0, 3.0, 1e6])
+@pytest.mark.parametrize("N,D,V", [(40, 64, 100003), (9, 1088, 100100), (300, 96, 60001)])
+def test_lse_of_exact_logits(N, D, V, T):
+    """On a binary grid every partial sum of a logit is exact in fp32, so only
+    the log-sum-exp's own roundings are left, none of which may grow with the
+    number of columns folded.  With R = 2^-22 (exp2's relative error) and
+    U = U32, the sum's relative error is at most
+      3 U ln V      the argument of exp2 is rounded and its scale twice: 3 U of
+                    a term's distance (M - z) / T, whose mean is below ln V
+      R             exp2
+      (64 + 16) U   additions: at most 64 chunks of 32 to a share, 9 within one, and
+                    the shares' (in more bits)
+      (R + 2 U) n   a new maximum rescales: n of them at most
+      R + 2 U       the shares' join
+    and the result is rounded once."""
+    import torch
+    import linear_cross_entropy_05_b200 as L
+    # the temperature is a float: 1e-3 stands for one 4.7e-8 larger (relatively),
+    # which alone moves an lse of 30900 by 1.5e-3
+    T = float(np.float32(T))
+    g = torch.Generator().manual_seed(N + D)
+    se, sc, K = 2.0 ** -5, 2.0 ** -11, 5
+    E = ((torch.randn(N, D, generator=g) / se).round() * se).to(torch.bfloat16)
+    C = ((torch.randn(V, D, generator=g) * (6.0 / D ** 0.5) / sc).round() * sc).to(torch.bfloat16)
+    z = (E.double() @ C.double().T).numpy()
+    assert (E.abs().double() @ C[:500].abs().double().T).max() * 1.5 < 2.0 ** 24 * se * sc
+    ids = torch.randint(0, V, (N, K), generator=g)
+    ids[:, 0] = torch.from_numpy(z.argmax(axis=1))
+    t = torch.randn(N, K, generator=g)
+    x = z / T
+    top = x.max(axis=1)
+    lse = top + np.log(np.exp(x - top[:, None]).sum(axis=1))
+    p, _ = oracle.distill_targets(ids.numpy(), f64(t), T, IGN)
+    q = np.take_along_axis(x, ids.numpy(), 1) - lse[:, None]
+    loss = T * T * (np.where(p > 0, p * np.log(np.maximum(p, 1e-300)), 0.0) - p * q).sum(axis=1)
+    R, U = 2.0 ** -22, U32
+    dlse = 3 * U * np.log(V) + R + 80 * U + (R + 2 * U) * records(z, 8) + R + 2 * U
+    got, gl = L.distill_forward(*(a.cuda() for a in (E, C, ids, t)), temperature=T)
+    err = np.abs(gl.double().cpu().numpy() - lse)
+    assert (err <= dlse + 1.01 * U * np.abs(lse)).all(), (err / (dlse + U * np.abs(lse))).max()
+    # the loss: lse before it is rounded, each weight rounded once, one rounding
+    # of the result (and T to float for T^2: 2 U)
+    err = np.abs(got.double().cpu().numpy() - loss)
+    bound = T * T * (dlse + U * (p * np.abs(q)).sum(axis=1)) + 4 * U * np.abs(loss) + 4 * U * T * np.abs(p * q).sum(axis=1) * T
+    assert (err <= bound).all(), (err / bound).max()
