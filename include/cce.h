@@ -370,7 +370,8 @@ CCE_API cce_status_t cce_distill_forward(const void* E, const void* C, const int
  * E, lse and dloss hold for a row without a gradient is not looked at.  lse is
  * cce_distill_forward's on the same inputs and temperature.  flags:
  * CCE_BWD_DETERMINISTIC (dE summed in stripe order; dC always is), CCE_BWD_BF16_GRADS,
- * CCE_BWD_ACCUMULATE, with their meaning in cce_backward_ex. */
+ * CCE_BWD_ACCUMULATE, with their meaning in cce_backward_ex.  If a bounded wait
+ * gave up, dE and dC are NaN. */
 CCE_API cce_status_t cce_distill_backward(const void* E, const void* C, const int64_t* ids, const void* teacher,
                                           int teacher_dtype, const float* lse, const float* dloss,
                                           int dloss_stride, const float* dloss_scale, int64_t N, int64_t D,

@@ -47,8 +47,9 @@ cudaError_t launch_flat_rows(const void* E, const void* C, const int64_t* y, con
 cudaError_t launch_f32_to_bf16(const float* src, void* dst, size_t n, bool accumulate, int sms, cudaStream_t stream);
 cudaError_t launch_distill_targets(const TargetArgs& a, cudaStream_t stream);
 cudaError_t launch_distill_finalize(const DistillFinArgs& a, cudaStream_t stream);
-cudaError_t launch_distill_parts(const float* parts, int n_parts, size_t part_floats, void* out, size_t n, bool bf16,
-                                 bool accumulate, int sms, cudaStream_t stream);
+cudaError_t launch_distill_parts(const float* parts, int n_parts, size_t part_floats, const GradOuts& o, size_t n,
+                                 bool bf16, bool accumulate, int sms, cudaStream_t stream);
+cudaError_t launch_distill_mark(const GradOuts& o, int sms, cudaStream_t stream);
 int head_logits_stages(int nt);
 cudaError_t launch_head_logits(const CUtensorMap& tmC, const CUtensorMap& tmC32, const CUtensorMap& tmE,
                                const HeadArgs& a, int grid, cudaStream_t stream);
@@ -1297,18 +1298,19 @@ cce_status_t cce_distill_backward(const void* E, const void* C, const int64_t* i
   st = backward_stripes(ws + L.off_E, C, dE32, dC_sum, bp, a, acc32, (flags & CCE_BWD_DETERMINISTIC) != 0, di.sms, ws, stream,
                         nullptr, &tg, temperature, L.dC_direct);
   if (st != CCE_OK) return st;
-  if (parts > 1) {
-    if (launch_distill_parts(dE32, parts, (size_t)part_rows(N) * D, dE, (size_t)N * D, bf16, accumulate, di.sms,
-                             stream) != cudaSuccess)
-      return CCE_ERR_CUDA;
-  } else if (bf16 &&
-             launch_f32_to_bf16(dE32, dE, (size_t)N * D, accumulate, di.sms, stream) != cudaSuccess) {
+  const size_t size = bf16 ? 2 : 4;
+  const GradOuts outs{dE, dC, (size_t)N * D * size, (size_t)V * D * size, reinterpret_cast<unsigned long long*>(ws)};
+  if (bf16 && parts == 1 &&
+      launch_f32_to_bf16(dE32, dE, (size_t)N * D, accumulate, di.sms, stream) != cudaSuccess)
     return CCE_ERR_CUDA;
-  }
   if (bf16 && !L.dC_direct && launch_f32_to_bf16(reinterpret_cast<const float*>(dC_sum), dC, (size_t)V * D, accumulate,
                                          di.sms, stream) != cudaSuccess)
     return CCE_ERR_CUDA;
-  return CCE_OK;
+  // (last, since it marks both gradients if a wait gave up)
+  const cudaError_t le = parts > 1 ? launch_distill_parts(dE32, parts, (size_t)part_rows(N) * D, outs, (size_t)N * D,
+                                                          bf16, accumulate, di.sms, stream)
+                                   : launch_distill_mark(outs, di.sms, stream);
+  return le == cudaSuccess ? CCE_OK : CCE_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -138,6 +138,15 @@ struct DistillFinArgs {
   float* inv_count;
 };
 
+// The gradients of a distillation backward and the status that tells whether a
+// wait gave up on them.
+struct GradOuts {
+  void* dE;
+  void* dC;
+  size_t dE_bytes, dC_bytes;  // multiples of 16
+  const unsigned long long* status;
+};
+
 // The head's logits of a chunk of tokens and the choice among them (head.cu).
 constexpr int HEAD_ROWS = 512;  // tokens per chunk
 constexpr int HEAD_EXP_TAB = 1024;

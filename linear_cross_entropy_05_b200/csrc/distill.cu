@@ -21,6 +21,10 @@
 //                  that finishes last adds up the mean, in a fixed order.
 // distill_parts    adds up dE from the parts that few tokens' stripes leave
 //                  (deterministic mode), in the order of the parts.
+// distill_mark     NaN to the gradients of a backward in which a bounded wait
+//                  gave up: tiles that were not reached hold what was there
+//                  before (distill_parts does it too, which saves few tokens'
+//                  calls a launch).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -222,10 +226,29 @@ __global__ void __launch_bounds__(32 * FIN_PARTS) distill_finalize_kernel(const 
   }
 }
 
+// If a wait gave up: NaN to both gradients (a pattern of both types).
+__device__ __forceinline__ bool mark_if_failed(const GradOuts& o) {
+  if (!(__ldcg(o.status + ST_FLAGS) & SF_TIMEOUT)) return false;
+  const uint4 nan4 = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
+  const size_t stride = (size_t)gridDim.x * blockDim.x, i0 = (size_t)blockIdx.x * blockDim.x + threadIdx.x;
+  for (size_t i = i0; i < o.dE_bytes / 16; i += stride) reinterpret_cast<uint4*>(o.dE)[i] = nan4;
+  for (size_t i = i0; i < o.dC_bytes / 16; i += stride) reinterpret_cast<uint4*>(o.dC)[i] = nan4;
+  return true;
+}
+
+__global__ void __launch_bounds__(256) distill_mark_kernel(const GradOuts o) { mark_if_failed(o); }
+
+cudaError_t launch_distill_mark(const GradOuts& o, int sms, cudaStream_t stream) {
+  distill_mark_kernel<<<sms, 256, 0, stream>>>(o);
+  return cudaGetLastError();
+}
+
 // dE = the sum of the parts (plus dE itself with `accumulate`), in their order.
 // part4: float4s from one part to the next.
 __global__ void __launch_bounds__(256) distill_parts_kernel(const float4* __restrict__ parts, int n_parts, size_t part4,
-                                                            void* out, size_t n4, int bf16, int accumulate) {
+                                                            const GradOuts o, size_t n4, int bf16, int accumulate) {
+  if (mark_if_failed(o)) return;
+  void* out = o.dE;
   const size_t stride = (size_t)gridDim.x * blockDim.x;
   for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n4; i += stride) {
     float4 v = __ldg(parts + i);
@@ -241,9 +264,9 @@ __global__ void __launch_bounds__(256) distill_parts_kernel(const float4* __rest
     } else {
       uint2* dst = reinterpret_cast<uint2*>(out) + i;
       if (accumulate) {
-        const uint2 o = *dst;
-        const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&o.x));
-        const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&o.y));
+        const uint2 old = *dst;
+        const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&old.x));
+        const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&old.y));
         v = make_float4(v.x + a.x, v.y + a.y, v.z + b.x, v.w + b.y);
       }
       const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
@@ -252,11 +275,11 @@ __global__ void __launch_bounds__(256) distill_parts_kernel(const float4* __rest
   }
 }
 
-cudaError_t launch_distill_parts(const float* parts, int n_parts, size_t part_floats, void* out, size_t n, bool bf16,
-                                 bool accumulate, int sms, cudaStream_t stream) {
+cudaError_t launch_distill_parts(const float* parts, int n_parts, size_t part_floats, const GradOuts& o, size_t n,
+                                 bool bf16, bool accumulate, int sms, cudaStream_t stream) {
   const size_t blocks = (n / 4 + 255) / 256;
   distill_parts_kernel<<<(unsigned)(blocks < (size_t)sms * 8 ? blocks : (size_t)sms * 8), 256, 0, stream>>>(
-      reinterpret_cast<const float4*>(parts), n_parts, part_floats / 4, out, n / 4, bf16 ? 1 : 0, accumulate ? 1 : 0);
+      reinterpret_cast<const float4*>(parts), n_parts, part_floats / 4, o, n / 4, bf16 ? 1 : 0, accumulate ? 1 : 0);
   return cudaGetLastError();
 }
 

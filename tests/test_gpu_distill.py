@@ -496,3 +496,37 @@ def test_lse_of_exact_logits(N, D, V, T):
     err = np.abs(got.double().cpu().numpy() - loss)
     bound = T * T * (dlse + U * (p * np.abs(q)).sum(axis=1)) + 4 * U * np.abs(loss) + 4 * U * T * np.abs(p * q).sum(axis=1) * T
     assert (err <= bound).all(), (err / bound).max()
+
+
+@pytest.mark.parametrize("D", [256, 264])
+@pytest.mark.parametrize("how", [dict(), dict(bf16_grads=True), dict(deterministic=True), dict(accumulate=True),
+                                 dict(bf16_grads=True, accumulate=True)])
+def test_a_backward_whose_wait_gives_up_yields_nan(D, how):
+    import torch
+    import linear_cross_entropy_05_b200 as L
+    N, V, K = 300, 5000, 20
+    E, C, ids, t, dl = [x.cuda() for x in make(62, N, D, V, K)]
+    gdt = torch.bfloat16 if how.get("bf16_grads") else torch.float32
+    ws = L.Workspace("cuda")
+    _, lse = L.distill_forward(E, C, ids, t, workspace=ws)
+
+    def call():
+        out = tuple(torch.zeros(s, dtype=gdt, device="cuda") for s in ((N, D), (V, D)))
+        return L.distill_backward(E, C, ids, t, lse, dl, workspace=ws, out=out, **how)
+
+    want = call()
+    assert L.read_status(ws)["status"] == 0
+    L.cce_debug_set_wait_limit_ns(20_000_000)
+    L.cce_debug_withhold_loads(True)
+    try:
+        got = call()
+        torch.cuda.synchronize()
+    finally:
+        L.cce_debug_withhold_loads(False)
+        L.cce_debug_set_wait_limit_ns(1_000_000_000)
+    assert L.read_status(ws)["status"] == 6
+    assert all(torch.isnan(g).all() for g in got)
+    got = call()
+    assert L.read_status(ws)["status"] == 0
+    for a, b in zip(got, want):
+        assert torch.isfinite(a).all() and (a.float() - b.float()).norm() <= U16 * b.float().norm()
