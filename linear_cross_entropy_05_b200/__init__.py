@@ -15,11 +15,12 @@ forward(E, C, y) -> (loss, lse), backward(E, C, y, lse, dloss, filter_eps)
 -> (dE, dC), and linear_cross_entropy(E, C, y) for a mean-reduced loss with
 autograd.
 
-On the same head, also without N x V logits in memory: distill_forward,
-distill_backward and linear_distillation (the loss on a teacher's top logits
-and its gradients; cce_distill_forward, cce_distill_backward), top_logits (the
-k largest logits per token; cce_top_logits) and sample (one drawn token per
-row; cce_sample).
+On the same head: distill_forward, distill_backward and linear_distillation
+(the loss on a teacher's top logits and its gradients, also without N x V
+logits in memory; cce_distill_forward, cce_distill_backward), and, with the
+logits of up to 512 tokens at a time in the workspace, top_logits (the k
+largest logits per token; cce_top_logits) and sample (one drawn token per row;
+cce_sample).
 """
 from __future__ import annotations
 

@@ -27,6 +27,13 @@
 //               this does not settle (more than kCap candidates: a wide
 //               nucleus, a row full of ties) take exact passes over the row.
 //
+// A logit is one accumulator's sum over all of D, whose truncated additions
+// leave the largest 8e-6 short (relatively) at D = 8192.  The distillation
+// forward hands its accumulator over every 1024 of D; here a thread would have
+// to hold 64 sums beside the 96 registers that 576 threads leave it, and parts
+// kept in tensor memory for few tokens only would make a token's logits depend
+// on how many others are in the call.
+//
 // A drawn token is decided by comparing u with a quotient of sums of up to V
 // exponentials; these sums are formed in double (a group's 32 in 2^-51
 // fixed point, so that no order of summation shows), because float sums would

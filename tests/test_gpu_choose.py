@@ -345,3 +345,41 @@ def test_min_p_of_one_at_temperatures_that_level_the_masses(V):
         for s in (dict(min_p=1.0), dict(min_p=1.0, top_k=12), dict(min_p=1.0, top_p=0.5)):
             s["temperature"] = t
             check_draw(L.sample(E.cuda(), C.cuda(), u.cuda(), **s), z, u, s)
+
+
+@pytest.mark.parametrize("D", [136, 896, 2304, 8192])
+def test_ordinary_inputs(D):
+    """Inputs on no grid: the tensor cores add 16 products at a time to a fp32
+    sum, D / 16 additions that each truncate by at most one step (2 U32) of the
+    sum of the magnitudes S, so a logit is off by at most
+    dz = (D / 16 + 1) 2 U32 S; log-sum-exps by that and FLOAT_SUMS."""
+    import torch
+    import linear_cross_entropy_05_b200 as L
+    N, V, k = 70, 9001, 40
+    g = torch.Generator().manual_seed(D)
+    E = torch.randn(N, D, generator=g).to(torch.bfloat16)
+    C = (torch.randn(V, D, generator=g) * 2.0 / D ** 0.5).to(torch.bfloat16)
+    for i in range(N):   # a few candidates stand out, as in a trained head
+        E[i] = (E[i].float() + 3.0 * C[7 * i:7 * i + 3].float().sum(0)).to(torch.bfloat16)
+    z = (E.double() @ C.double().T).numpy()
+    dz = ((D / 16 + 1) * 2 * U32 * (E.double().abs() @ C.double().abs().T)).numpy()
+    most = dz.max(axis=1)
+    top = z.max(axis=1)
+    wide = np.log(np.exp(z - top[:, None]).sum(axis=1))       # lse - largest
+    dlse = most + FLOAT_SUMS * wide + 1.01 * U32 * np.abs(top + wide) + 1e-12
+    values, ids, lse = (t.cpu().numpy() for t in L.top_logits(E.cuda(), C.cuda(), k))
+    rows = np.arange(N)[:, None]
+    assert (np.abs(values - z[rows, ids]) <= dz[rows, ids] + U32 * np.abs(values)).all()
+    assert (np.diff(values, axis=1) <= 0).all()
+    kth = np.sort(z, axis=1)[:, -k]
+    assert all(np.unique(r).size == k for r in ids) and (z[rows, ids] >= (kth - 2 * most)[:, None]).all()
+    assert (np.abs(lse - (top + wide)) <= dlse).all()
+    u = torch.rand(N, generator=g).cuda()
+    token, logp = (t.cpu().numpy() for t in L.sample(E.cuda(), C.cuda(), u, temperature=0.0))
+    assert np.array_equal(token, ids[:, 0])
+    got = z[np.arange(N), token]
+    assert (np.abs(logp - (got - top - wide)) <= 2 * most + dlse).all()
+    token, logp = (t.cpu().numpy() for t in L.sample(E.cuda(), C.cuda(), u, top_k=k, top_p=0.9))
+    assert all(token[i] in ids[i] for i in range(N))
+    got = z[np.arange(N), token]
+    assert (np.abs(logp - (got - top - wide)) <= 2 * most + dlse).all()
