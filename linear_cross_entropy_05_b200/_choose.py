@@ -11,7 +11,7 @@ import torch
 
 from . import Workspace
 from ._distill import Launch, check_head, check_tensor
-from ._native import CCESampleSettings, cce_head_workspace_size, cce_sample, cce_top_logits
+from ._native import CCEError, CCESampleSettings, cce_head_workspace_size, cce_sample, cce_top_logits
 
 
 def top_logits(E, C, k: int, workspace: Optional[Workspace] = None, stream=None, out=None):
@@ -21,9 +21,11 @@ def top_logits(E, C, k: int, workspace: Optional[Workspace] = None, stream=None,
     distill_forward takes of a teacher.  k is at most 1024 (and V).  The
     scratch holds the logits of min(N, 512) tokens."""
     N, D, V = check_head(E, C)
+    if not 0 < k <= min(V, 1024):      # (before anything of its size is allocated)
+        raise CCEError(1, f"cce_top_logits: k must be in 1 .. min(V, 1024), not {k}")
     with Launch(E.device, stream, workspace) as run:
         if out is None:
-            values, ids = run.empty((N, max(k, 0)), torch.float32), run.empty((N, max(k, 0)), torch.int64)
+            values, ids = run.empty((N, k), torch.float32), run.empty((N, k), torch.int64)
             lse = run.empty((N,), torch.float32)
         else:
             values, ids, lse = out
@@ -31,8 +33,8 @@ def top_logits(E, C, k: int, workspace: Optional[Workspace] = None, stream=None,
             check_tensor(ids, "ids", (N, k), torch.int64, E.device)
             check_tensor(lse, "lse", (N,), torch.float32, E.device)
         ws = run.scratch(cce_head_workspace_size(N, D, V), "cce_head_workspace_size")
-        cce_top_logits(E.data_ptr(), C.data_ptr(), N, D, V, k, values.data_ptr() if k > 0 else ws.data_ptr(),
-                       ids.data_ptr() if k > 0 else ws.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.numel(), run.ptr)
+        cce_top_logits(E.data_ptr(), C.data_ptr(), N, D, V, k, values.data_ptr(), ids.data_ptr(), lse.data_ptr(),
+                       ws.data_ptr(), ws.numel(), run.ptr)
     return values, ids, lse
 
 

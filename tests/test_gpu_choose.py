@@ -383,3 +383,30 @@ def test_ordinary_inputs(D):
     assert all(token[i] in ids[i] for i in range(N))
     got = z[np.arange(N), token]
     assert (np.abs(logp - (got - top - wide)) <= 2 * most + dlse).all()
+
+
+def test_a_k_out_of_range_allocates_nothing():
+    import torch
+    import linear_cross_entropy_05_b200 as L
+    E, C, _, _ = make(53, 6, 64, 300)
+    E, C = E.cuda(), C.cuda()
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    held = torch.cuda.memory_allocated()
+    for k in (301, 1 << 24, 1 << 50, -(1 << 50)):
+        with pytest.raises(L.CCEError):
+            L.top_logits(E, C, k)
+    assert torch.cuda.max_memory_allocated() == held
+
+
+def test_a_token_is_chosen_alike_in_any_batch():
+    import torch
+    import linear_cross_entropy_05_b200 as L
+    g = torch.Generator().manual_seed(54)
+    N, D, V = 600, 2304, 9001
+    E = torch.randn(N, D, generator=g).to(torch.bfloat16).cuda()
+    C = (torch.randn(V, D, generator=g) * 3.0 / D ** 0.5).to(torch.bfloat16).cuda()
+    values, ids, _ = L.top_logits(E, C, 50)
+    for rows in ([0], [599], list(range(100, 133)), list(range(0, 600, 2)), list(range(40, 552))):
+        v, i, _ = L.top_logits(E[rows].contiguous(), C, 50)
+        assert torch.equal(v, values[rows]) and torch.equal(i, ids[rows])
