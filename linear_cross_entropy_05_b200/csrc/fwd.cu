@@ -396,16 +396,16 @@ cudaError_t read_l2_halves(unsigned* out, int n) {
 // ----------------------------------------------------------------------------
 // PICK_SLICES (long rows of E): the tensor cores round every addition into an
 // accumulator towards zero, about D / 16 times a logit, which leaves a D = 4096
-// head's largest logits, and with them the loss, 3e-6 short (relatively; 5e-6
-// at 8192).  A divergence may itself be small beside the log-sum-exp it is
+// head's largest logits 4e-6 short (relatively; 8e-6 at 8192), and the loss 2e-6
+// (6e-6) off.  A divergence may itself be small beside the log-sum-exp it is
 // formed from, so here the accumulator is handed over every kSliceSteps * 64 of
 // D, and the parts are added in registers, rounded to nearest: eight epilogue
 // warps, two per lane group, hold 128 columns each while the next part is being
 // formed.  Loss error and time, whole -> in parts of 1024:
-//   1000 x 2048 x 128256   1.4e-6 -> 6.7e-7   401 -> 418 us
-//   2048 x 4096 x 128256   2.9e-6 -> 6.5e-7   1383 -> 1425 us
-//   4096 x 2304 x 256000   1.5e-6 -> 5.7e-7   3030 -> 3183 us
-// (parts of 512: 3e-7, another 3 %).
+//   1000 x 2048 x 128256   1.1e-6 -> 5.2e-7   408 -> 430 us
+//   2048 x 4096 x 128256   2.1e-6 -> 5.1e-7   1385 -> 1441 us
+//   4096 x 2304 x 256000   8.2e-7 -> 3.4e-7   3058 -> 3236 us
+// (parts of 512: another 3 %).
 constexpr int kSliceSteps = 16;
 enum PickKind : int { PICK_NONE = 0, PICK_WHOLE = 1, PICK_SLICES = 2 };
 template <int PICK>
